@@ -113,7 +113,8 @@ typedef struct {
 
 /* ABI version of this header (bumped on any change to the entry points;
  * 3 added the 8-bit calls and qr_check_wait_timeout, 4 the FP4 calls, 5
- * qr_w4a4_linear_fused, 6 qr_w4a4_linear_fused_noalloc). */
+ * qr_w4a4_linear_fused, 6 qr_w4a4_linear_fused_noalloc).  The calls on
+ * qr_kv_cache came later without a bump: they change no entry point of 6. */
 #define QR_ABI_VERSION 6
 QR_API int32_t qr_abi_version(void);
 
@@ -404,6 +405,153 @@ QR_API qr_status qr_kv_quantize(const uint16_t* Q, const uint16_t* K, const uint
                                 uint16_t* q_rot, uint8_t* k_codes, float* k_scales,
                                 int32_t* k_zeros, uint8_t* v_codes, float* v_scales,
                                 int32_t* v_zeros, qr_stream stream);
+
+/* ----------------------------------------------------------------------
+ * Serving from the 4-bit KV cache.  The pages quantize keys and values
+ * (qr_kv_quantize) and leave their consumer to the model; these calls are that
+ * consumer: the write into a paged cache behind the rotary embedding, the
+ * read back, the attention over the cache, the attention weight each cached token
+ * has received (the statistic that eviction goes by), and eviction.
+ *
+ * Cache.  Six arrays of `slots` rows, one row per token slot, in the layout
+ * qr_kv_quantize writes: codes uint8 [slots x W/2] (W = heads * head_dim,
+ * element 2j in the low nibble, two's complement), scales float32 and zeros int32
+ * [slots x W/group]; a value is scale * (code - zero).  Keys stand in the basis of
+ * R3.  head_dim in {32, 64, 128, 256}; group 128 or 256, a multiple of head_dim
+ * that divides W; W <= 65536; codes 16-byte aligned, scales and zeros 4-byte.
+ * The rows are pages of page_size slots; a tail of slots that fills no page
+ * is never used.
+ *
+ * Sequences.  Token t of sequence b lies in slot
+ * page(b, t / page_size) * page_size + t % page_size, where page(b, p) is
+ * block_table[b * max_pages + p], or b * max_pages + p without a table.  kv_lens[b]
+ * tokens are held (those of the call included); cu_q[b] .. cu_q[b + 1] are the
+ * rows of the call's query or token arrays that belong to sequence b: its newest
+ * tokens, in order.  kv_lens, cu_q and block_table are device arrays, read by the
+ * kernels when they run, so that a captured graph sees their current values.
+ * Lengths below 0 count as 0 and those above max_pages * page_size as that.  A page
+ * number outside the cache is never followed: tokens there are not written, not
+ * attended to and read back as 0.  Rows outside [cu_q[0], cu_q[batch]) and outside
+ * the arrays are not touched.  Pages may be shared between sequences for reading;
+ * a page that two sequences (or two places of one) write in one call is
+ * left with some mixture of the two.
+ * batch <= 4096, max_pages * page_size < 2^30. */
+typedef struct {
+  uint8_t* k_codes;
+  float* k_scales;
+  int32_t* k_zeros;
+  uint8_t* v_codes;
+  float* v_scales;
+  int32_t* v_zeros;
+  int64_t slots;             /* rows of each array */
+  int32_t heads;             /* key/value heads */
+  int32_t head_dim;
+  int32_t group;
+  int32_t page_size;         /* slots per page, >= 1 */
+} qr_kv_cache;
+
+typedef struct {
+  int32_t batch;
+  int32_t max_pages;           /* pages a sequence may have */
+  const int32_t* block_table;  /* [batch x max_pages], or NULL */
+  const int32_t* kv_lens;      /* [batch] */
+  const int32_t* cu_q;         /* [batch + 1]; may be NULL for qr_kv_evict */
+} qr_kv_seqs;
+
+/* Rotary embedding with one or several position axes (text: one; images and
+ * video: time, height, width).  Pair i < pairs of every head turns by the angle
+ * positions[axis[i] * ld_pos + row] * inv_freq[i], formed and reduced in double
+ * precision; an axis outside [0, axes) leaves its pair as it is.  The pair is
+ * elements (i, i + pairs), or (2 i, 2 i + 1) when interleaved; elements from
+ * 2 * pairs on are left as they are.  With c and s the cosine and sine rounded to
+ * float32: (a, b) -> (a c - b s, b c + a s), each operation rounded to float32. */
+typedef struct {
+  const float* inv_freq;       /* [pairs] */
+  const int32_t* axis;         /* [pairs], or NULL: every pair on axis 0 */
+  const int32_t* positions;    /* [axes x ld_pos], ld_pos >= tokens */
+  int64_t ld_pos;
+  int32_t pairs;               /* 1 <= pairs <= head_dim / 2 */
+  int32_t axes;                /* >= 1 */
+  int32_t interleaved;
+} qr_kv_rope;
+
+/* Rope and R3 on the rows of Q and K, fp16 queries out, 4-bit codes of K and V
+ * into the cache at the sequences' newest places.
+ *  rope   host struct, or NULL: the rows carry their positions already
+ *  Q      fp16 [tokens x ldq], q_heads * head_dim wide (a multiple of group);
+ *         q_rot fp16 [tokens x q_heads * head_dim]; both NULL: no queries
+ *  K, V   fp16 [tokens x ldk], [tokens x ldv], W wide; NULL: that side of the
+ *         cache is left as it is
+ * Without a rope the results equal qr_kv_quantize's bit for bit.  Pointers
+ * 16-byte aligned, ldq, ldk, ldv multiples of 8 (ALIGNMENT otherwise).  q_rot must not overlap
+ * Q.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA. */
+QR_API qr_status qr_kv_append(const qr_kv_cache* cache, const qr_kv_seqs* seqs,
+                              const qr_kv_rope* rope, const uint16_t* Q, int64_t ldq,
+                              const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv,
+                              int64_t tokens, int32_t q_heads, uint16_t* q_rot, qr_stream stream);
+
+/* The values scale * (code - zero) of the sequences' newest tokens, rounded to
+ * fp16: k_out, v_out fp16 [tokens x W] (either may be NULL), 16-byte aligned.  Keys
+ * come in the basis of R3, as the cache holds them. */
+QR_API qr_status qr_kv_dequantize(const qr_kv_cache* cache, const qr_kv_seqs* seqs, int64_t tokens,
+                                  uint16_t* k_out, uint16_t* v_out, qr_stream stream);
+
+/* Attention over the cache.  Row i of sequence b (i < new_b = cu_q[b+1] - cu_q[b]),
+ * query head h of q_heads = G * heads, reads key head h / G:
+ *   x_t = scale * q . k_t,   o = sum_t softmax(x)_t v_t,   lse = log(sum_t exp(x_t))
+ * over the tokens t < n, with n = kv_lens[b] - new_b + i + 1 when causal (the rows are
+ * the newest tokens; none are seen when that is <= 0) and n = kv_lens[b] otherwise
+ * (cross attention: new_b and kv_lens[b] are unrelated).  A row that sees no key gets
+ * o = 0, lse = -inf.
+ *  Q      fp16 [tokens x ldq] with R3 applied (qr_kv_append, qr_kv_quantize)
+ *  out    fp16 [tokens x ldo]; lse float32 [tokens x q_heads], or NULL
+ *  Q and out 16-byte aligned, ldq and ldo multiples of 8
+ *  workspace   device memory, 16-byte aligned, of at least
+ *         qr_kv_attention_workspace() bytes; its contents do not matter before
+ *         and after the call, and calls that may run at the same time need one each
+ * Scores, the softmax's maximum and sum and the output's sums are fp32; the weights
+ * that meet the values on the tensor cores are rounded to fp16 (a pair of fp16
+ * where few rows share a key).
+ * scale finite; q_heads a multiple of heads, q_heads * head_dim <= 65536. */
+QR_API int64_t qr_kv_attention_workspace(const qr_kv_cache* cache, const qr_kv_seqs* seqs,
+                                         int64_t tokens, int32_t q_heads);
+QR_API qr_status qr_kv_attention(const qr_kv_cache* cache, const qr_kv_seqs* seqs,
+                                 const uint16_t* Q, int64_t ldq, int64_t tokens, int32_t q_heads,
+                                 float scale, int32_t causal, uint16_t* out, int64_t ldo,
+                                 float* lse, void* workspace, int64_t workspace_bytes,
+                                 qr_stream stream);
+
+/* The attention weight that each cached token receives from the rows of a call,
+ * added to a running sum, per quantization group (the heads of a group share
+ * their scales and are evicted together):
+ *   mass[(b * W/group + j) * ld_mass + t] += sum over the rows i of sequence b and the query
+ *                         heads of group j of exp(scale * q . k_t - lse)  (t visible to i)
+ * lse as qr_kv_attention writes it for the same rows; rows with lse = -inf add
+ * nothing.  mass float32, ld_mass >= max_pages * page_size.  The order of the sum is
+ * fixed: equal calls give equal bits. */
+QR_API qr_status qr_kv_attention_mass(const qr_kv_cache* cache, const qr_kv_seqs* seqs,
+                                      const uint16_t* Q, int64_t ldq, int64_t tokens,
+                                      int32_t q_heads, float scale, int32_t causal,
+                                      const float* lse, float* mass, int64_t ld_mass,
+                                      qr_stream stream);
+
+/* Eviction by accumulated mass, per sequence and group.  Of n = kv_lens[b] tokens,
+ * when n > keep, the newest `recent` stay, and of the others the keep - recent with the
+ * largest mass (equal masses: the lower slot; NaN counts as -inf); they move, in
+ * order, to the first keep places.  When n <= keep all stay.
+ *  table_out   int32 [batch x max_pages]: the pages that receive the tokens, all
+ *              different from the pages being read; NULL: in place (pages that two
+ *              sequences share must not be compacted in place)
+ *  mass        as above; mass_out [.. x ld_mass]: the mass of the kept tokens, moved
+ *              along, and 0 from there to ld_mass; may be `mass` itself
+ *  kept        int32 [batch x W/group x keep]: the place each kept token had, -1
+ *              behind the last
+ *  lens_out    int32 [batch]: min(n, keep); not kv_lens itself
+ * 1 <= keep < 2^30, 0 <= recent <= keep.  cu_q is not used. */
+QR_API qr_status qr_kv_evict(const qr_kv_cache* cache, const qr_kv_seqs* seqs, const float* mass,
+                             int64_t ld_mass, int32_t keep, int32_t recent,
+                             const int32_t* table_out, float* mass_out, int32_t* kept,
+                             int32_t* lens_out, qr_stream stream);
 
 /* Codes a kernel records in the device status word when one of its bounded
  * waits runs out (the role that gave up); 0 = nothing recorded. */

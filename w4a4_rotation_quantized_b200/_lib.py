@@ -20,7 +20,9 @@ EXPORTED = ("qr_abi_version", "qr_status_string", "qr_packed_k", "qr_rotate_quan
             "qr_weight_code_sums", "qr_w4a4_linear_asym", "qr_kv_quantize",
             "qr_check_wait_timeout", "qr_rotate_quant8", "qr_pack_weights8", "qr_w8a8_linear",
             "qr_rotate_quant_fp4", "qr_pack_weights_fp4", "qr_fp4_linear",
-            "qr_w4a4_linear_fused", "qr_w4a4_linear_fused_noalloc")
+            "qr_w4a4_linear_fused", "qr_w4a4_linear_fused_noalloc", "qr_kv_append",
+            "qr_kv_dequantize", "qr_kv_attention_workspace", "qr_kv_attention",
+            "qr_kv_attention_mass", "qr_kv_evict")
 
 # codes of the device status word (qr_device_status)
 QR_DEV_TIMEOUT_GRID_SYNC = 0x106
@@ -40,6 +42,47 @@ class QrRotation(ctypes.Structure):
         ("chan_mode", ctypes.c_int32),
         ("clip_ratio", ctypes.c_float),
         ("signs", ctypes.c_void_p),
+    ]
+
+
+class QrKvCache(ctypes.Structure):
+    """Mirror of the C struct qr_kv_cache."""
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("k_zeros", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("v_zeros", ctypes.c_void_p),
+        ("slots", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+    ]
+
+
+class QrKvSeqs(ctypes.Structure):
+    """Mirror of the C struct qr_kv_seqs."""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p),
+        ("cu_q", ctypes.c_void_p),
+    ]
+
+
+class QrKvRope(ctypes.Structure):
+    """Mirror of the C struct qr_kv_rope."""
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p),
+        ("axis", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("ld_pos", ctypes.c_int64),
+        ("pairs", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
     ]
 
 
@@ -97,6 +140,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "qr_w4a4_linear_fused_noalloc": (ctypes.c_int, [rot_p, vp, i64, i64, i64, vp, i32, vp, vp,
                                                         vp, vp, i64, i32, vp, i64, vp]),
     }
+    cache_p, seqs_p = ctypes.POINTER(QrKvCache), ctypes.POINTER(QrKvSeqs)
+    f32 = ctypes.c_float
+    sig.update({
+        "qr_kv_append": (ctypes.c_int, [cache_p, seqs_p, ctypes.POINTER(QrKvRope), vp, i64, vp, i64,
+                                        vp, i64, i64, i32, vp, vp]),
+        "qr_kv_dequantize": (ctypes.c_int, [cache_p, seqs_p, i64, vp, vp, vp]),
+        "qr_kv_attention_workspace": (i64, [cache_p, seqs_p, i64, i32]),
+        "qr_kv_attention": (ctypes.c_int, [cache_p, seqs_p, vp, i64, i64, i32, f32, i32, vp, i64, vp,
+                                           vp, i64, vp]),
+        "qr_kv_attention_mass": (ctypes.c_int, [cache_p, seqs_p, vp, i64, i64, i32, f32, i32, vp, vp,
+                                                i64, vp]),
+        "qr_kv_evict": (ctypes.c_int, [cache_p, seqs_p, vp, i64, i32, i32, vp, vp, vp, vp, vp]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -289,4 +345,51 @@ def qr_w4a4_linear_fused_noalloc(rot, X, M, K, ldx, outlier_idx, n_out, w_codes,
                                              stream)
     if check:
         _check("qr_w4a4_linear_fused_noalloc", st)
+    return st
+
+
+def qr_kv_append(cache, seqs, rope, Q, ldq, K, ldk, V, ldv, tokens, q_heads, q_rot, stream, *,
+                 check=True):
+    st = load().qr_kv_append(cache, seqs, rope, Q, ldq, K, ldk, V, ldv, tokens, q_heads, q_rot,
+                             stream)
+    if check:
+        _check("qr_kv_append", st)
+    return st
+
+
+def qr_kv_dequantize(cache, seqs, tokens, k_out, v_out, stream, *, check=True):
+    st = load().qr_kv_dequantize(cache, seqs, tokens, k_out, v_out, stream)
+    if check:
+        _check("qr_kv_dequantize", st)
+    return st
+
+
+def qr_kv_attention_workspace(cache, seqs, tokens, q_heads) -> int:
+    return load().qr_kv_attention_workspace(cache, seqs, tokens, q_heads)
+
+
+def qr_kv_attention(cache, seqs, Q, ldq, tokens, q_heads, scale, causal, out, ldo, lse, workspace,
+                    workspace_bytes, stream, *, check=True):
+    st = load().qr_kv_attention(cache, seqs, Q, ldq, tokens, q_heads, scale, causal, out, ldo, lse,
+                                workspace, workspace_bytes, stream)
+    if check:
+        _check("qr_kv_attention", st)
+    return st
+
+
+def qr_kv_attention_mass(cache, seqs, Q, ldq, tokens, q_heads, scale, causal, lse, mass, ld_mass,
+                         stream, *, check=True):
+    st = load().qr_kv_attention_mass(cache, seqs, Q, ldq, tokens, q_heads, scale, causal, lse, mass,
+                                     ld_mass, stream)
+    if check:
+        _check("qr_kv_attention_mass", st)
+    return st
+
+
+def qr_kv_evict(cache, seqs, mass, ld_mass, keep, recent, table_out, mass_out, kept, lens_out,
+                stream, *, check=True):
+    st = load().qr_kv_evict(cache, seqs, mass, ld_mass, keep, recent, table_out, mass_out, kept,
+                            lens_out, stream)
+    if check:
+        _check("qr_kv_evict", st)
     return st

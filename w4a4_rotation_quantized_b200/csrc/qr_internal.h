@@ -137,6 +137,53 @@ qr_status launch_kv_group_quant(const uint16_t* src, int64_t groups, int group, 
 qr_status launch_code_row_sums(const uint8_t* codes, int64_t rows, int64_t kp, int32_t* sums,
                                cudaStream_t stream);
 
+// The calls on the paged 4-bit KV cache (arguments checked by qr_kv_api.cu).
+struct KvView;
+struct KvAppendJob {
+  const qr_kv_rope* rope;     // or null
+  const uint16_t *q, *k, *v;  // each may be null
+  int64_t ldq, ldk, ldv;
+  int32_t q_heads;
+  uint16_t* q_rot;
+};
+struct KvAttentionJob {
+  const uint16_t* q;
+  int64_t ldq;
+  int32_t q_heads;
+  float scale;
+  int32_t causal;
+  uint16_t* out;
+  int64_t ldo;
+  float* lse;                 // or null
+  void* workspace;
+};
+struct KvMassJob {
+  const uint16_t* q;
+  int64_t ldq;
+  int32_t q_heads;
+  float scale;
+  int32_t causal;
+  const float* lse;
+  float* mass;
+  int64_t ld_mass;
+};
+struct KvEvictJob {
+  const float* mass;
+  int64_t ld_mass;
+  int32_t keep, recent;
+  const int32_t* table_out;   // null: in place
+  float* mass_out;
+  int32_t* kept;
+  int32_t* lens_out;
+};
+qr_status launch_kv_append(const KvView& v, const KvAppendJob& job, cudaStream_t stream);
+qr_status launch_kv_dequantize(const KvView& v, uint16_t* k_out, uint16_t* v_out,
+                               cudaStream_t stream);
+int64_t kv_attention_workspace(const KvView& v, int32_t q_heads);
+qr_status launch_kv_attention(const KvView& v, const KvAttentionJob& job, cudaStream_t stream);
+qr_status launch_kv_mass(const KvView& v, const KvMassJob& job, cudaStream_t stream);
+qr_status launch_kv_evict(const KvView& v, const KvEvictJob& job, cudaStream_t stream);
+
 // One thread waits, with the given limit, on an mbarrier nothing arrives on.
 qr_status launch_wait_selfcheck(uint64_t limit_ns, cudaStream_t stream);
 
