@@ -1,163 +1,611 @@
-// kv_attention.cu -- attention over the paged 4-bit KV cache, and the attention
-// weight that each cached token receives.
+// kv_attention.cu -- attention over the paged 4-bit KV cache for few query rows
+// a key head (single tokens, drafts): every code is read once from memory, so the bytes of the
+// cache bound it, H_k (d + 16 d / g) a token.
 //
-// One warp per (row, query head), its lanes over the head's elements: for each
-// visible token the score is a warp sum, and the running maximum m, sum l and
-// output o of the softmax are carried along,
-//   m' = max(m, x),  l' = l e^(m - m') + e^(x - m'),  o' = o e^(m - m') + e^(x - m') v.
-// The mass kernel turns this around: one warp per (sequence, group, token), which
-// sums e^(x - lse) over the rows that see the token.
+// S^T = K Q^T and O^T += V^T W^T on the warp matrix instructions, tokens and output elements in the 16
+// rows, 8 (or 16) query rows in the columns: with the queries as rows most of the products would be padding.
+// Codes become fp16 operands in registers (kv_mma.cuh); the scales meet the scores and the weights:
+//   x_t = s_k (sum q u - z' sum q) scale log2 e,   z' = z + 8, u = c + 8
+//   o   = sum w_t (c - z),   w_t = s_v 2^(x_t - m),   l = sum 2^(x_t - m).
+// The running maximum m is that of x_t + log2 s_v (with log2 s_v held to [-40, 40]): then the weights that are
+// rounded for the matrix instructions are at most 1 and those that matter are near 1, whatever the values'
+// scales are, and one factor rescales l and o alike.  A weight goes in as two fp16, its rounding and the
+// rest: the matrix instructions have room for that (1.5 a token and head).  Zeros of values beyond +-900,
+// which c - z would not survive in fp16, leave a remainder that is summed apart.
+//
+// A warp takes one key head and 32 tokens at a time, its own ring of such pieces in shared
+// memory, filled by asynchronous copies ahead of their use; warps of a block take neighbouring heads
+// of the same tokens (scales of 8 heads share a sector) and do not wait for each other.  With
+// fewer heads than warps, warps share a head's tokens and join at the end of an item.
+// Work is shared out by kv_split.cuh.
+#include <algorithm>
 #include <cmath>
 
-#include "kv_device.cuh"
+#include "kv_mma.cuh"
+#include "kv_split.cuh"
 #include "qr_internal.h"
 
 namespace qr {
 
 namespace {
 
-// Values of a lane's E elements of head h in slot `slot`.
-template <int E>
-__device__ __forceinline__ void load_values(const KvView& v, int side, int64_t slot, int h, int lane,
-                                            float (&x)[E]) {
-  const int e = h * v.head_dim + lane * E;
-  const int64_t g = slot * v.groups + e / v.group;
-  const float s = v.scales[side][g];
-  const int32_t z = v.zeros[side][g];
-  const uint8_t* c = v.codes[side] + slot * (v.width / 2);
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+// pieces of a warp's ring: with three of them two blocks fit an SM (one, and two pieces, where a
+// head is 256 wide)
+template <int D>
+constexpr int stages() { return D == 256 ? 2 : 3; }
+constexpr int kStep = 32;                      // tokens of a piece
+
+struct SplitArgs {
+  KvView v;
+  SplitPlan plan;
+  const __half* q;
+  int64_t ldq;
+  int32_t q_heads;
+  float scale_log2;                            // scale * log2 e
+  __half* out;
+  int64_t ldo;
+  float* lse;
+  int64_t* prefix;                             // [batch + 1]
+  float2* part_ml;                             // [2 blocks][heads of a block][rows]
+  float* part_o;                               // ... [D]
+  int32_t heads_log2;                          // heads of a block = 2^heads_log2
+};
+
+// A part's place: slot 0 holds the part that begins a block's range, slot 1 one that ends it.
+__device__ __forceinline__ int64_t part_at(const SplitArgs& a, int32_t block, int slot, int head, int row) {
+  return (((static_cast<int64_t>(block) * 2 + slot) << a.heads_log2) + head) * a.plan.rows + row;
+}
+
+// Writes N fp16 values of a finished row.
+template <int N>
+__device__ __forceinline__ void store_half(__half* to, const float (&x)[N]) {
+  __half2 h[N / 2];
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const int nib = (c[(e + j) >> 1] >> (4 * ((e + j) & 1))) & 0xF;
-    x[j] = s * static_cast<float>(static_cast<int64_t>((nib ^ 8) - 8) - z);
+  for (int i = 0; i < N / 2; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+  if constexpr (N >= 8) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(h)[i];
+  } else {
+    *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(h);
   }
 }
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
+__device__ __forceinline__ float inverse_or_zero(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
-// Tokens that row i of a sequence sees.
-__device__ __forceinline__ int32_t visible(int32_t len, int32_t rows, int32_t i, int causal) {
-  return causal ? min(max(len - rows + i + 1, 0), len) : len;
-}
+template <int D, int NC>
+constexpr int ring_bytes() { return kWarps * (stages<D>() * KvStage<D>::kBytes + KvStage<D>::kPrepared); }
+template <int D, int NC>
+constexpr int join_bytes() { return kWarps * 8 * NC * (D + 2) * 4; }
+template <int D, int NC>
+constexpr int tile_bytes() { return ring_bytes<D, NC>() > join_bytes<D, NC>() ? ring_bytes<D, NC>() : join_bytes<D, NC>(); }
 
-template <int E>
-__global__ void __launch_bounds__(256) kv_attention_kernel(KvView v, const __half* Q, int64_t ldq,
-                                                           int32_t q_heads, float scale, int causal,
-                                                           __half* out, int64_t ldo, float* lse) {
+template <int D, int NC>
+__global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_split_kernel(const SplitArgs a) {
+  using S = KvStage<D>;
+  using T = ValueTile<D>;
+  constexpr int R = 8 * NC, kStages = stages<D>();
+  extern __shared__ __align__(128) uint8_t smem[];
+  const KvView& v = a.v;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  const int hb = 1 << a.heads_log2, hw = warp & (hb - 1), sw = warp >> a.heads_log2;
+  const int ws = kWarps >> a.heads_log2;               // warps of a head
+  uint8_t* ring = smem + warp * (kStages * S::kBytes + S::kPrepared);
+  float* prep_rest = reinterpret_cast<float*>(ring + kStages * S::kBytes);         // [32]
+  __half* prep_z = reinterpret_cast<__half*>(prep_rest + 32);                      // [32]
+  const uint32_t ring_u32 = smem_u32(ring);
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem + tile_bytes<D, NC>());
+
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  const int64_t job = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int32_t i = static_cast<int32_t>(job / q_heads), h = static_cast<int32_t>(job % q_heads);
-  if (i >= v.tokens) return;
-  const int32_t b = kv_seq_of_row(v, i);
-  if (b >= v.batch) return;
-  const int32_t c0 = v.cu[b], c1 = v.cu[b + 1];
-  if (i < c0 || c0 < 0) return;
-  const int32_t n = visible(kv_len(v, b), c1 - c0, i - c0, causal);
-  const int hk = h / (q_heads / v.heads);
-  float q[E], o[E], x[E], m = -INFINITY, l = 0.0f;
+  split_prefix<kThreads>(v, a.plan, prefix);
+  const int64_t units = prefix[v.batch];
+  if (blockIdx.x == 0)
+    for (int32_t b = threadIdx.x; b <= v.batch; b += kThreads) a.prefix[b] = prefix[b];
+  const int64_t start = range_start(a.plan, units, blockIdx.x);
+  const int64_t end = range_start(a.plan, units, blockIdx.x + 1);
+
+  int32_t b = 0;
+  for (int64_t at = start; at < end;) {
+    // the item that unit `at` belongs to
+    {
+      int32_t lo = b, hi = v.batch - 1;                 // the last b with prefix[b] <= at
+      while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= at) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
+    }
+    const SeqRows rows = seq_rows(v, b);
+    int64_t off = at - prefix[b];
+    int32_t tile = 0, tu = tile_units(a.plan, rows, 0);
+    while (off >= static_cast<int64_t>(tu) * a.plan.head_blocks) {
+      off -= static_cast<int64_t>(tu) * a.plan.head_blocks;
+      tu = tile_units(a.plan, rows, ++tile);
+    }
+    const int32_t block = static_cast<int32_t>(off / tu), u0 = static_cast<int32_t>(off % tu);
+    const int32_t take = static_cast<int32_t>(min(static_cast<int64_t>(tu - u0), end - at));
+    const int head = (block << a.heads_log2) + hw;
+    const int32_t n_seen = tile_seen(a.plan, rows, tile);
+
+    // queries of this tile: row r is new token r / gq, head r % gq of the group
+    const int32_t row0 = tile * R, all_rows = rows.here * a.plan.gq;
+    QueryFrag<D> q[NC];
+    uint64_t qsum[NC];
+    int32_t limit[NC][2], all_limit = n_seen;           // all_limit: seen by every row
+    bool has[NC][2];
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    q[j] = __half2float(Q[i * ldq + h * 32 * E + lane * E + j]);
-    o[j] = 0.0f;
+    for (int n = 0; n < NC; ++n) {
+      const int32_t r = row0 + 8 * n + g;
+      const __half* from = nullptr;
+      if (r < all_rows)
+        from = a.q + (rows.first + r / a.plan.gq) * a.ldq +
+               static_cast<int64_t>(head * a.plan.gq + r % a.plan.gq) * D;
+      float s = q[n].load(from, c);
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      qsum[n] = f2_pack(__shfl_sync(0xffffffffu, s, 8 * c), __shfl_sync(0xffffffffu, s, 8 * c + 4));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int32_t rr = row0 + 8 * n + 2 * c + e;
+        has[n][e] = rr < all_rows;
+        limit[n][e] = has[n][e] ? seen(rows, rr / a.plan.gq, a.plan.causal) : 0;
+      }
+    }
+    if (a.plan.causal) all_limit = seen(rows, row0 / a.plan.gq, 1);
+
+    uint64_t o[T::kTiles][NC][2], l2[NC];                // pairs: columns 2c, 2c + 1
+#pragma unroll
+    for (int i = 0; i < T::kTiles; ++i)
+#pragma unroll
+      for (int n = 0; n < NC; ++n) o[i][n][0] = o[i][n][1] = 0;
+    float m[NC][2], zs[NC][2];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      l2[n] = 0;
+      m[n][0] = m[n][1] = -INFINITY;
+      zs[n][0] = zs[n][1] = 0.0f;
+    }
+
+    // this warp's pieces: tokens first + 32 ws i
+    const int32_t first = (u0 * ws + sw) * kStep;
+    auto slot_of = [&](int32_t i) -> int32_t {
+      const int32_t t = first + i * ws * kStep + lane;
+      return i < take && t < n_seen ? static_cast<int32_t>(kv_slot(v, v.table, b, t)) : -1;
+    };
+    uint32_t there[kStages];                            // tokens that are, of the pieces in flight
+    int32_t slot = slot_of(0);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      const int32_t next = slot_of(i + 1);
+      there[i] = __ballot_sync(0xffffffffu, slot >= 0);
+      if (i < take) S::template issue<true, true>(v, head, slot, ring_u32 + i * S::kBytes, lane);
+      cp_async_commit();
+      slot = next;
+    }
+    int stage = 0, fill = kStages - 1;
+    for (int32_t i = 0; i < take; ++i) {
+      const int32_t next = slot_of(i + kStages);
+      there[kStages - 1] = __ballot_sync(0xffffffffu, slot >= 0);
+      if (i + kStages - 1 < take)
+        S::template issue<true, true>(v, head, slot, ring_u32 + fill * S::kBytes, lane);
+      cp_async_commit();
+      slot = next;
+      fill = fill + 1 == kStages ? 0 : fill + 1;
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      const uint8_t* st = ring + stage * S::kBytes;
+      const int32_t t0 = first + i * ws * kStep;
+      // each lane makes one token's numbers ready for all, in place of the four it came with
+      float4* prep = reinterpret_cast<float4*>(ring + stage * S::kBytes + S::kMeta);
+      bool rest;
+      {
+        const float* meta = reinterpret_cast<const float*>(prep);
+        const int32_t zv = __float_as_int(meta[96 + lane]), zc = min(max(zv, -900), 900);
+        const float sk = meta[lane] * (a.scale_log2 * 16777216.0f);
+        const float zk = (static_cast<float>(__float_as_int(meta[32 + lane])) + 8.0f) * -0x1p-24f;
+        const float sv = meta[64 + lane], lv = fminf(fmaxf(__log2f(sv), -40.0f), 40.0f);
+        __syncwarp();
+        prep[lane] = make_float4(sk, zk, lv, sv);
+        prep_z[lane] = __int2half_rn(-1032 - zc);
+        rest = __any_sync(0xffffffffu, zv != zc);
+        if (rest) prep_rest[lane] = static_cast<float>(static_cast<int64_t>(zv) - zc);
+        __syncwarp();
+      }
+      float x[2][NC][4], top[NC][2];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) top[n][0] = top[n][1] = -INFINITY;
+      const bool clear = there[0] == 0xffffffffu && t0 + kStep <= all_limit;   // every row sees every token
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float hi[NC][4];
+        key_scores<D, NC>(st, 16 * h, g, c, q, x[h], hi);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {                     // tokens g and g + 8
+          const int t = 16 * h + 8 * e + g;
+          const float4 k = prep[t];
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            float* y = &x[h][n][2 * e];
+            const uint64_t sum = f2_fma(f2_pack(hi[n][2 * e], hi[n][2 * e + 1]), f2_pack(0.0625f, 0.0625f),
+                                        f2_pack(y[0], y[1]));
+            f2_unpack(f2_mul(f2_fma(f2_pack(k.y, k.y), qsum[n], sum), f2_pack(k.x, k.x)), y[0], y[1]);
+            if (!clear) {
+              const bool is = (there[0] >> t) & 1u;
+              if (!(is && t0 + t < limit[n][0])) y[0] = -INFINITY;
+              if (!(is && t0 + t < limit[n][1])) y[1] = -INFINITY;
+            }
+            float y0, y1;
+            f2_unpack(f2_add(f2_pack(y[0], y[1]), f2_pack(k.z, k.z)), y0, y1);
+            top[n][0] = fmaxf(top[n][0], y0);
+            top[n][1] = fmaxf(top[n][1], y1);
+          }
+        }
+      }
+      bool grown = false;
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) top[n][k] = fmaxf(top[n][k], __shfl_xor_sync(0xffffffffu, top[n][k], s));
+          grown |= top[n][k] > m[n][k];
+        }
+      if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          float f[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float m1 = fmaxf(m[n][k], top[n][k]);
+            f[k] = m[n][k] == m1 ? 1.0f : exp2_fast(m[n][k] - m1);
+            m[n][k] = m1;
+            zs[n][k] *= f[k];
+          }
+          const uint64_t f2 = f2_pack(f[0], f[1]);
+          l2[n] = f2_mul(l2[n], f2);
+#pragma unroll
+          for (int j = 0; j < T::kTiles; ++j) {
+            o[j][n][0] = f2_mul(o[j][n][0], f2);
+            o[j][n][1] = f2_mul(o[j][n][1], f2);
+          }
+        }
+      }
+      uint64_t m0[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        m0[n] = f2_pack(m[n][0] == -INFINITY ? 0.0f : -m[n][0], m[n][1] == -INFINITY ? 0.0f : -m[n][1]);
+      uint32_t wh[2][NC][2], wl[2][NC][2], z1024[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 16 * h + 8 * e + g;
+          const float sv = prep[t].w;
+          z1024[h][e] = *reinterpret_cast<const uint32_t*>(prep_z + 16 * h + 8 * e + 2 * c);
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            float p0, p1, w0, w1;
+            f2_unpack(f2_add(f2_pack(x[h][n][2 * e], x[h][n][2 * e + 1]), m0[n]), p0, p1);
+            const uint64_t p = f2_pack(exp2_fast(p0), exp2_fast(p1));
+            l2[n] = f2_add(l2[n], p);
+            f2_unpack(f2_mul(p, f2_pack(sv, sv)), w0, w1);
+            if (!clear) {                                  // a scale that is not seen may be anything
+              if (x[h][n][2 * e] == -INFINITY) w0 = 0.0f;
+              if (x[h][n][2 * e + 1] == -INFINITY) w1 = 0.0f;
+            }
+            if (rest) {
+              const float r = prep_rest[t];
+              zs[n][0] = fmaf(w0, r, zs[n][0]);
+              zs[n][1] = fmaf(w1, r, zs[n][1]);
+            }
+            const __half2 hi = __floats2half2_rn(w0, w1);
+            const float2 back = __half22float2(hi);
+            float r0, r1;
+            f2_unpack(f2_sub(f2_pack(w0, w1), f2_pack(back.x, back.y)), r0, r1);
+            const __half2 lo = __floats2half2_rn(r0, r1);
+            wh[h][n][e] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&hi));
+            wl[h][n][e] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&lo));
+          }
+        }
+      }
+      value_products<D, NC>(st + S::kCodes, g, c, z1024, wh, wl, o);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+#pragma unroll
+      for (int s = 0; s + 1 < kStages; ++s) there[s] = there[s + 1];
+      __syncwarp();
+    }
+    cp_async_wait<0>();
+
+    float l[NC][2];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) f2_unpack(l2[n], l[n][0], l[n][1]);
+    // sums of column k of product j, row g or g + 8, without the remainder
+    auto sum_of = [&](int j, int n, int k, bool upper) {
+      float y[2];
+      f2_unpack(o[j][n][upper], y[0], y[1]);
+      return y[k] - zs[n][k];
+    };
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) {
+          l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], s);
+          zs[n][k] += __shfl_xor_sync(0xffffffffu, zs[n][k], s);
+        }
+    const bool whole = take == tu;
+    const int part = at == start ? 0 : 1;
+    if (ws == 1) {
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (!has[n][k]) continue;
+          const int32_t r = 8 * n + 2 * c + k, rr = row0 + r;
+          const float inv = whole ? inverse_or_zero(l[n][k]) : 1.0f;
+          float y[T::kPer];
+#pragma unroll
+          for (int j = 0; j < T::kTiles; ++j) {
+            y[T::element(j, false)] = sum_of(j, n, k, false) * inv;
+            y[T::element(j, true)] = sum_of(j, n, k, true) * inv;
+          }
+          if (whole) {
+            const int64_t token = rows.first + rr / a.plan.gq;
+            const int h = head * a.plan.gq + rr % a.plan.gq;
+            store_half(a.out + token * a.ldo + h * D + g * T::kPer, y);
+            if (a.lse != nullptr && g == 0) a.lse[token * a.q_heads + h] = row_lse(m[n][k], l[n][k]);
+          } else {
+            const int64_t p = part_at(a, blockIdx.x, part, hw, r);
+            float4* to = reinterpret_cast<float4*>(a.part_o + p * D + g * T::kPer);
+#pragma unroll
+            for (int j = 0; j < T::kPer / 4; ++j) to[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+            if (g == 0) a.part_ml[p] = make_float2(m[n][k], l[n][k]);
+          }
+        }
+    } else {
+      // the warps of a head meet: rows of D sums, m and l in shared memory
+      __syncthreads();
+      float* mine = reinterpret_cast<float*>(smem) + warp * R * (D + 2);
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float* to = mine + (8 * n + 2 * c + k) * (D + 2);
+#pragma unroll
+          for (int j = 0; j < T::kTiles; ++j) {
+            to[g * T::kPer + T::element(j, false)] = sum_of(j, n, k, false);
+            to[g * T::kPer + T::element(j, true)] = sum_of(j, n, k, true);
+          }
+          if (g == 0) {
+            to[D] = m[n][k];
+            to[D + 1] = l[n][k];
+          }
+        }
+      __syncthreads();
+      const float* all = reinterpret_cast<const float*>(smem);
+      for (int e = threadIdx.x; e < (R << a.heads_log2) * (D / 2); e += kThreads) {
+        const int d2 = e % (D / 2) * 2, hr = e / (D / 2), r = hr % R, h0 = hr / R;
+        const int32_t rr = row0 + r;
+        if (rr >= all_rows) continue;
+        float mm = -INFINITY;
+        for (int s = 0; s < ws; ++s) mm = fmaxf(mm, all[((s << a.heads_log2) + h0) * R * (D + 2) + r * (D + 2) + D]);
+        float ll = 0.0f, y0 = 0.0f, y1 = 0.0f;
+        for (int s = 0; s < ws; ++s) {
+          const float* from = all + ((s << a.heads_log2) + h0) * R * (D + 2) + r * (D + 2);
+          const float f = from[D] == mm ? 1.0f : exp2_fast(from[D] - mm);
+          ll = fmaf(from[D + 1], f, ll);
+          y0 = fmaf(from[d2], f, y0);
+          y1 = fmaf(from[d2 + 1], f, y1);
+        }
+        if (whole) {
+          const float inv = inverse_or_zero(ll);
+          const int64_t token = rows.first + rr / a.plan.gq;
+          const int h = ((block << a.heads_log2) + h0) * a.plan.gq + rr % a.plan.gq;
+          *reinterpret_cast<__half2*>(a.out + token * a.ldo + h * D + d2) = __floats2half2_rn(y0 * inv, y1 * inv);
+          if (a.lse != nullptr && d2 == 0) a.lse[token * a.q_heads + h] = row_lse(mm, ll);
+        } else {
+          const int64_t p = part_at(a, blockIdx.x, part, h0, r);
+          *reinterpret_cast<float2*>(a.part_o + p * D + d2) = make_float2(y0, y1);
+          if (d2 == 0) a.part_ml[p] = make_float2(mm, ll);
+        }
+      }
+      __syncthreads();
+    }
+    at += take;
   }
-  for (int32_t t = 0; t < n; ++t) {
-    const int64_t slot = kv_slot(v, v.table, b, t);
-    if (slot < 0) continue;
-    load_values<E>(v, 0, slot, hk, lane, x);
-    float dot = 0.0f;
-#pragma unroll
-    for (int j = 0; j < E; ++j) dot = fmaf(q[j], x[j], dot);
-    dot = warp_sum(dot) * scale;
-    const float m1 = fmaxf(m, dot);
-    const float keep = expf(m - m1), p = expf(dot - m1);
-    load_values<E>(v, 1, slot, hk, lane, x);
-#pragma unroll
-    for (int j = 0; j < E; ++j) o[j] = fmaf(o[j], keep, p * x[j]);
-    l = fmaf(l, keep, p);
-    m = m1;
-  }
-  const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;      // NaN stays
-#pragma unroll
-  for (int j = 0; j < E; ++j)
-    out[i * ldo + h * 32 * E + lane * E + j] = __float2half_rn(o[j] * inv);
-  if (lse != nullptr && lane == 0)
-    lse[static_cast<int64_t>(i) * q_heads + h] = l == 0.0f ? -INFINITY : m + logf(l);
 }
 
-template <int E>
-__global__ void __launch_bounds__(256) kv_mass_kernel(KvView v, const __half* Q, int64_t ldq,
-                                                      int32_t q_heads, float scale, int causal,
-                                                      const float* lse, float* mass,
-                                                      int64_t ld_mass) {
+// Adds up the parts of the rows whose items were cut.  One group of JW warps a (token, query head): its
+// warps take every JW-th part, lanes the elements of the head.
+template <int D, int JW>
+__global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
+  constexpr int E = D / 32;
+  constexpr int kGroups = 8 / JW;
+  __shared__ float acc[kGroups][JW > 1 ? JW : 1][D];
+  __shared__ float2 ml[kGroups][JW > 1 ? JW : 1];
+  const KvView& v = a.v;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp / JW, jw = warp % JW;
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  const int32_t b = blockIdx.z, j = blockIdx.y;
-  const int32_t t = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int32_t len = kv_len(v, b);
-  if (t >= len) return;
-  const int64_t slot = kv_slot(v, v.table, b, t);
-  if (slot < 0) return;
-  const int32_t c0 = max(v.cu[b], 0), c1 = min(v.cu[b + 1], v.tokens);
-  const int per = v.group / v.head_dim, gq = q_heads / v.heads;
-  float sum = 0.0f;
-  for (int hk = j * per; hk < (j + 1) * per; ++hk) {
-    float x[E];
-    load_values<E>(v, 0, slot, hk, lane, x);
-    for (int32_t i = c0; i < c1; ++i) {
-      if (t >= visible(len, v.cu[b + 1] - v.cu[b], i - v.cu[b], causal)) continue;
-      for (int h = hk * gq; h < (hk + 1) * gq; ++h) {
-        float dot = 0.0f;
+  const int64_t job = static_cast<int64_t>(blockIdx.x) * kGroups + grp;
+  const int32_t i = static_cast<int32_t>(job / a.q_heads), h = static_cast<int32_t>(job % a.q_heads);
+  bool work = i < v.tokens;
+  int32_t b = v.batch;
+  if (work) b = kv_seq_of_row(v, i);
+  work = work && b < v.batch;
+  int32_t first = 0, last = 0, r = 0, hb = 0;
+  int64_t u0 = 0, units = 0;
+  if (work) {
+    const SeqRows rows = seq_rows(v, b);
+    const int32_t ti = i - rows.first;
+    work = ti >= 0 && ti < rows.here;
+    if (work) {
+      units = a.prefix[v.batch];
+      const int hk = h / a.plan.gq;
+      const int64_t row = static_cast<int64_t>(ti) * a.plan.gq + h % a.plan.gq;
+      const int32_t tile = static_cast<int32_t>(row / a.plan.rows);
+      r = static_cast<int32_t>(row % a.plan.rows);
+      hb = hk & ((1 << a.heads_log2) - 1);
+      u0 = a.prefix[b];
+      for (int32_t t = 0; t < tile; ++t) u0 += static_cast<int64_t>(tile_units(a.plan, rows, t)) * a.plan.head_blocks;
+      const int32_t tu = tile_units(a.plan, rows, tile);
+      u0 += static_cast<int64_t>(hk >> a.heads_log2) * tu;
+      first = max(range_of(a.plan, units, u0), 0);
+      last = min(range_of(a.plan, units, u0 + tu - 1), a.plan.blocks - 1);
+      work = first < last;
+    }
+  }
+  if (JW == 1 && !work) return;                          // (JW > 1: the block meets below)
+  float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          dot = fmaf(__half2float(Q[i * ldq + h * 32 * E + lane * E + e]), x[e], dot);
-        dot = warp_sum(dot) * scale;
-        const float ls = lse[static_cast<int64_t>(i) * q_heads + h];
-        sum += ls == -INFINITY ? 0.0f : expf(dot - ls);
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  if (work) {
+    // 32 parts at a time: their m and l, one a lane, then their sums, eight in flight
+    for (int32_t c0 = first; c0 <= last; c0 += 32 * JW) {
+      const int32_t blk = c0 + lane * JW + jw;
+      int64_t p = 0;
+      float2 x = make_float2(-INFINITY, 0.0f);
+      if (blk <= last) {
+        const int64_t s = range_start(a.plan, units, blk);
+        if (s < range_start(a.plan, units, blk + 1)) {
+          p = part_at(a, blk, s >= u0 ? 0 : 1, hb, r);
+          x = a.part_ml[p];
+        }
+      }
+      float top = x.x;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      const float m1 = fmaxf(m, top);
+      const float keep = m == m1 ? 1.0f : exp2_fast(m - m1);
+      const float f = x.x == m1 ? 1.0f : exp2_fast(x.x - m1);
+      // a part without a key (m = -inf) counts nothing; l tells (a row of NaN has one)
+      const float mine = x.y == 0.0f ? 0.0f : f;
+      float ls = x.y * mine;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+      l = fmaf(l, keep, ls);
+      m = m1;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= keep;
+      uint32_t left = __ballot_sync(0xffffffffu, x.y != 0.0f);
+      while (left != 0) {
+        float f8[8], y[8][E];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int from = left != 0 ? __ffs(left) - 1 : -1;
+          left &= left - 1;
+          const int64_t pk = __shfl_sync(0xffffffffu, p, max(from, 0));
+          f8[k] = __shfl_sync(0xffffffffu, mine, max(from, 0));
+          const float* src = a.part_o + pk * D;
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[k][e] = from >= 0 ? src[e * 32 + lane] : 0.0f;
+          if (from < 0) f8[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(y[k][e], f8[k], o[e]);
       }
     }
   }
-  if (lane == 0) mass[(static_cast<int64_t>(b) * v.groups + j) * ld_mass + t] += sum;
+  if (JW > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[grp][jw][e * 32 + lane] = o[e];
+    if (lane == 0) ml[grp][jw] = make_float2(m, l);
+    __syncthreads();
+    if (!work || jw != 0) return;
+    for (int w = 0; w < JW; ++w) m = fmaxf(m, ml[grp][w].x);
+    l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int w = 0; w < JW; ++w) {
+      const float2 x = ml[grp][w];
+      const float f = x.y == 0.0f ? 0.0f : x.x == m ? 1.0f : exp2_fast(x.x - m);
+      l = fmaf(x.y, f, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(acc[grp][w][e * 32 + lane], f, o[e]);
+    }
+  }
+  const float inv = inverse_or_zero(l);
+#pragma unroll
+  for (int e = 0; e < E; ++e) a.out[i * a.ldo + h * D + e * 32 + lane] = __float2half_rn(o[e] * inv);
+  if (a.lse != nullptr && lane == 0) a.lse[static_cast<int64_t>(i) * a.q_heads + h] = row_lse(m, l);
+}
+
+struct SplitSizes {
+  int nc, heads_log2, blocks;
+  int64_t prefix_bytes, ml_bytes, bytes;
+};
+
+SplitSizes split_sizes(const KvView& v, int32_t q_heads) {
+  SplitSizes s{};
+  const int gq = q_heads / v.heads;
+  const int64_t rows = (static_cast<int64_t>(v.tokens) * gq + v.batch - 1) / v.batch;   // of a sequence, on average
+  s.nc = rows > 8 && v.head_dim <= 128 ? 2 : 1;
+  while (s.heads_log2 < 3 && v.heads % (2 << s.heads_log2) == 0) ++s.heads_log2;
+  s.blocks = sm_count() * (v.head_dim == 256 || s.nc == 2 ? 1 : 2);
+  s.prefix_bytes = (8 * (static_cast<int64_t>(v.batch) + 1) + 255) / 256 * 256;
+  const int64_t parts = (2ll * s.blocks << s.heads_log2) * 8 * s.nc;
+  s.ml_bytes = parts * 8;
+  s.bytes = s.prefix_bytes + s.ml_bytes + parts * v.head_dim * 4;
+  return s;
+}
+
+template <int D, int NC>
+cudaError_t run_split(const SplitArgs& a, cudaStream_t stream) {
+  const size_t smem = tile_bytes<D, NC>() + (a.v.batch + 1) * sizeof(int64_t);
+  cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<D, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kv_split_kernel<D, NC>, dim3(a.plan.blocks), dim3(kThreads), smem, stream, 1, a);
+  if (e != cudaSuccess) return e;
+  // few rows share many parts: eight warps a row, else one
+  const int64_t rows = static_cast<int64_t>(a.v.tokens) * a.q_heads;
+  const int64_t items = std::max<int64_t>(1, static_cast<int64_t>(a.v.batch) * a.plan.head_blocks);
+  return a.plan.blocks > 4 * items
+             ? launch_pdl(kv_join_kernel<D, 8>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, stream, 1, a)
+             : launch_pdl(kv_join_kernel<D, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream,
+                          1, a);
 }
 
 }  // namespace
 
-int64_t kv_attention_workspace(const KvView& v, int32_t q_heads) {
-  (void)v;
-  (void)q_heads;
-  return 0;
-}
+int64_t kv_attention_workspace(const KvView& v, int32_t q_heads) { return split_sizes(v, q_heads).bytes; }
 
 qr_status launch_kv_attention(const KvView& v, const KvAttentionJob& j, cudaStream_t stream) {
-  const int64_t warps = static_cast<int64_t>(v.tokens) * j.q_heads;
-  const dim3 grid(static_cast<unsigned>((warps + 7) / 8)), block(256);
-  const auto* q = reinterpret_cast<const __half*>(j.q);
-  auto* out = reinterpret_cast<__half*>(j.out);
+  const SplitSizes s = split_sizes(v, j.q_heads);
+  SplitArgs a{};
+  a.v = v;
+  a.plan.gq = j.q_heads / v.heads;
+  a.plan.rows = 8 * s.nc;
+  a.plan.unit = kStep * (kWarps >> s.heads_log2);
+  a.plan.head_blocks = v.heads >> s.heads_log2;
+  a.plan.blocks = s.blocks;
+  a.plan.causal = j.causal;
+  a.q = reinterpret_cast<const __half*>(j.q);
+  a.ldq = j.ldq;
+  a.q_heads = j.q_heads;
+  a.scale_log2 = static_cast<float>(static_cast<double>(j.scale) * 1.4426950408889634);
+  a.out = reinterpret_cast<__half*>(j.out);
+  a.ldo = j.ldo;
+  a.lse = j.lse;
+  a.prefix = static_cast<int64_t*>(j.workspace);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(j.workspace) + s.prefix_bytes);
+  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(j.workspace) + s.prefix_bytes + s.ml_bytes);
+  a.heads_log2 = s.heads_log2;
   cudaError_t e;
   switch (v.head_dim) {
-    case 32: e = launch_pdl(kv_attention_kernel<1>, grid, block, 0, stream, 1, v, q, j.ldq, j.q_heads, j.scale, j.causal, out, j.ldo, j.lse); break;
-    case 64: e = launch_pdl(kv_attention_kernel<2>, grid, block, 0, stream, 1, v, q, j.ldq, j.q_heads, j.scale, j.causal, out, j.ldo, j.lse); break;
-    case 128: e = launch_pdl(kv_attention_kernel<4>, grid, block, 0, stream, 1, v, q, j.ldq, j.q_heads, j.scale, j.causal, out, j.ldo, j.lse); break;
-    default: e = launch_pdl(kv_attention_kernel<8>, grid, block, 0, stream, 1, v, q, j.ldq, j.q_heads, j.scale, j.causal, out, j.ldo, j.lse); break;
-  }
-  if (e == cudaSuccess) e = cudaGetLastError();
-  return e == cudaSuccess ? QR_OK : QR_ERR_CUDA;
-}
-
-qr_status launch_kv_mass(const KvView& v, const KvMassJob& j, cudaStream_t stream) {
-  const dim3 grid((v.capacity + 7) / 8, v.groups, v.batch), block(256);
-  const auto* q = reinterpret_cast<const __half*>(j.q);
-  cudaError_t e;
-  switch (v.head_dim) {
-    case 32: e = launch_pdl(kv_mass_kernel<1>, grid, block, 0, stream, 1, v, q, j.ldq, j.q_heads, j.scale, j.causal, j.lse, j.mass, j.ld_mass); break;
-    case 64: e = launch_pdl(kv_mass_kernel<2>, grid, block, 0, stream, 1, v, q, j.ldq, j.q_heads, j.scale, j.causal, j.lse, j.mass, j.ld_mass); break;
-    case 128: e = launch_pdl(kv_mass_kernel<4>, grid, block, 0, stream, 1, v, q, j.ldq, j.q_heads, j.scale, j.causal, j.lse, j.mass, j.ld_mass); break;
-    default: e = launch_pdl(kv_mass_kernel<8>, grid, block, 0, stream, 1, v, q, j.ldq, j.q_heads, j.scale, j.causal, j.lse, j.mass, j.ld_mass); break;
+    case 32: e = s.nc == 2 ? run_split<32, 2>(a, stream) : run_split<32, 1>(a, stream); break;
+    case 64: e = s.nc == 2 ? run_split<64, 2>(a, stream) : run_split<64, 1>(a, stream); break;
+    case 128: e = s.nc == 2 ? run_split<128, 2>(a, stream) : run_split<128, 1>(a, stream); break;
+    default: e = run_split<256, 1>(a, stream); break;
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? QR_OK : QR_ERR_CUDA;
