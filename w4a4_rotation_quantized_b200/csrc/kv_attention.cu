@@ -10,7 +10,8 @@
 // The running maximum m is that of x_t + log2 s_v (with log2 s_v held to [-40, 40]): then the weights that are
 // rounded for the matrix instructions are at most 1 and those that matter are near 1, whatever the values'
 // scales are, and one factor rescales l and o alike.  A weight goes in as two fp16, its rounding and the
-// rest: the matrix instructions have room for that (1.5 a token and head).  Zeros of values beyond +-900,
+// rest: the matrix instructions have room for that (1.5 a token and head).  The maximum is let lag: as long as no
+// weight passes 2^8 nothing is rescaled, and the warp need not even find its maximum.  Zeros of values beyond +-900,
 // which c - z would not survive in fp16, leave a remainder that is summed apart.
 //
 // A warp takes one key head and 32 tokens at a time, its own ring of such pieces in shared
@@ -20,6 +21,7 @@
 // Work is shared out by kv_split.cuh.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv_mma.cuh"
 #include "kv_split.cuh"
@@ -31,10 +33,9 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-// pieces of a warp's ring: with three of them two blocks fit an SM (one, and two pieces, where a
-// head is 256 wide)
+// pieces of a warp's ring
 template <int D>
-constexpr int stages() { return D == 256 ? 2 : 3; }
+constexpr int stages() { return 2; }
 constexpr int kStep = 32;                      // tokens of a piece
 
 struct SplitArgs {
@@ -78,7 +79,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 __device__ __forceinline__ float inverse_or_zero(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
 template <int D, int NC>
-constexpr int ring_bytes() { return kWarps * (stages<D>() * KvStage<D>::kBytes + KvStage<D>::kPrepared); }
+constexpr int ring_bytes() { return kWarps * (stages<D>() * KvStage<D>::kBytes + KvStage<D>::kPrepared + NC * QueryFrag<D>::kBytes); }
 template <int D, int NC>
 constexpr int join_bytes() { return kWarps * 8 * NC * (D + 2) * 4; }
 template <int D, int NC>
@@ -95,9 +96,12 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
   const int g = lane >> 2, c = lane & 3;
   const int hb = 1 << a.heads_log2, hw = warp & (hb - 1), sw = warp >> a.heads_log2;
   const int ws = kWarps >> a.heads_log2;               // warps of a head
-  uint8_t* ring = smem + warp * (kStages * S::kBytes + S::kPrepared);
-  float* prep_rest = reinterpret_cast<float*>(ring + kStages * S::kBytes);         // [32]
+  uint8_t* ring = smem + warp * (kStages * S::kBytes + S::kPrepared + NC * QueryFrag<D>::kBytes);
+  uint4* q = reinterpret_cast<uint4*>(ring + kStages * S::kBytes);                 // [NC][word][32]
+  float* prep_rest = reinterpret_cast<float*>(q + NC * QueryFrag<D>::kBytes / 16); // [32]
   __half* prep_z = reinterpret_cast<__half*>(prep_rest + 32);                      // [32]
+  uint32_t* piece_there = reinterpret_cast<uint32_t*>(prep_z + 32);                // [4]
+  int32_t* row_limit = reinterpret_cast<int32_t*>(piece_there + 4);                // [16]
   const uint32_t ring_u32 = smem_u32(ring);
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + tile_bytes<D, NC>());
 
@@ -107,11 +111,12 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
   const int64_t units = prefix[v.batch];
   if (blockIdx.x == 0)
     for (int32_t b = threadIdx.x; b <= v.batch; b += kThreads) a.prefix[b] = prefix[b];
-  const int64_t start = range_start(a.plan, units, blockIdx.x);
-  const int64_t end = range_start(a.plan, units, blockIdx.x + 1);
-
+  // this block's units, from the start of its range (a range has less than 2^31)
+  const int32_t count = static_cast<int32_t>(range_start(a.plan, units, blockIdx.x + 1) -
+                                             range_start(a.plan, units, blockIdx.x));
   int32_t b = 0;
-  for (int64_t at = start; at < end;) {
+  for (int32_t done = 0; done < count;) {
+    const int64_t at = range_start(a.plan, units, blockIdx.x) + done;
     // the item that unit `at` belongs to
     {
       int32_t lo = b, hi = v.batch - 1;                 // the last b with prefix[b] <= at
@@ -129,16 +134,14 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
       tu = tile_units(a.plan, rows, ++tile);
     }
     const int32_t block = static_cast<int32_t>(off / tu), u0 = static_cast<int32_t>(off % tu);
-    const int32_t take = static_cast<int32_t>(min(static_cast<int64_t>(tu - u0), end - at));
+    const int32_t take = min(tu - u0, count - done);
+    const bool whole = take == tu;
     const int head = (block << a.heads_log2) + hw;
     const int32_t n_seen = tile_seen(a.plan, rows, tile);
 
     // queries of this tile: row r is new token r / gq, head r % gq of the group
     const int32_t row0 = tile * R, all_rows = rows.here * a.plan.gq;
-    QueryFrag<D> q[NC];
-    uint64_t qsum[NC];
-    int32_t limit[NC][2], all_limit = n_seen;           // all_limit: seen by every row
-    bool has[NC][2];
+    float qsum[NC][2];
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       const int32_t r = row0 + 8 * n + g;
@@ -146,127 +149,114 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
       if (r < all_rows)
         from = a.q + (rows.first + r / a.plan.gq) * a.ldq +
                static_cast<int64_t>(head * a.plan.gq + r % a.plan.gq) * D;
-      float s = q[n].load(from, c);
+      float s = QueryFrag<D>::put(q + n * (D / 32) * 32, from, lane);
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
-      qsum[n] = f2_pack(__shfl_sync(0xffffffffu, s, 8 * c), __shfl_sync(0xffffffffu, s, 8 * c + 4));
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int32_t rr = row0 + 8 * n + 2 * c + e;
-        has[n][e] = rr < all_rows;
-        limit[n][e] = has[n][e] ? seen(rows, rr / a.plan.gq, a.plan.causal) : 0;
-      }
+      qsum[n][0] = __shfl_sync(0xffffffffu, s, 8 * c);
+      qsum[n][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
     }
-    if (a.plan.causal) all_limit = seen(rows, row0 / a.plan.gq, 1);
+    if (lane < R) row_limit[lane] = row0 + lane < all_rows ? seen(rows, (row0 + lane) / a.plan.gq, a.plan.causal) : 0;
+    const int32_t all_limit = seen(rows, row0 / a.plan.gq, a.plan.causal);      // seen by every row
 
-    uint64_t o[T::kTiles][NC][2], l2[NC];                // pairs: columns 2c, 2c + 1
+    uint64_t o[T::kTiles][NC][2], l2[NC];                // pairs of columns 2c, 2c + 1
+    float nm[NC][2];                                     // -m
 #pragma unroll
     for (int i = 0; i < T::kTiles; ++i)
 #pragma unroll
       for (int n = 0; n < NC; ++n) o[i][n][0] = o[i][n][1] = 0;
-    float m[NC][2], zs[NC][2];
+    float zs[NC][2];
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       l2[n] = 0;
-      m[n][0] = m[n][1] = -INFINITY;
-      zs[n][0] = zs[n][1] = 0.0f;
+      nm[n][0] = nm[n][1] = zs[n][0] = zs[n][1] = 0.0f;
     }
+    uint32_t started = 0;                                // bit 2 n + k: the column has seen a key
 
     // this warp's pieces: tokens first + 32 ws i
     const int32_t first = (u0 * ws + sw) * kStep;
+    const uint8_t* key = v.codes[0] + head * S::kRow + lane % S::kChunks * 16;
+    const uint8_t* value = v.codes[1] + head * S::kRow + lane % S::kChunks * 16;
+    const uint32_t group = head * D / v.group;
+    const int32_t page0 = b * v.max_pages;               // (batch * max_pages may not pass 2^31)
+    const int32_t* pages = v.table != nullptr ? v.table + page0 : nullptr;
     auto slot_of = [&](int32_t i) -> int32_t {
-      const int32_t t = first + i * ws * kStep + lane;
-      return i < take && t < n_seen ? static_cast<int32_t>(kv_slot(v, v.table, b, t)) : -1;
+      const int32_t t = first + i * ws * kStep + lane, tc = max(min(t, n_seen - 1), 0);
+      const int32_t p = kv_page(v, tc);
+      const int32_t page = pages != nullptr ? pages[p] : page0 + p;
+      return t < n_seen && static_cast<uint32_t>(page) < static_cast<uint32_t>(v.pages)
+                 ? page * v.page_size + (tc - p * v.page_size) : -1;
     };
-    uint32_t there[kStages];                            // tokens that are, of the pieces in flight
+    // starts piece i into a stage, whose last word says which of its tokens are there
+    auto fill = [&](int32_t i, int32_t slot, int stage) {
+      const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
+      if (lane == 0) piece_there[stage] = there;
+      if (i < take) S::template issue<true, true>(v, key, value, group, max(slot, 0), ring_u32 + stage * S::kBytes, lane);
+      cp_async_commit();
+    };
     int32_t slot = slot_of(0);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
       const int32_t next = slot_of(i + 1);
-      there[i] = __ballot_sync(0xffffffffu, slot >= 0);
-      if (i < take) S::template issue<true, true>(v, head, slot, ring_u32 + i * S::kBytes, lane);
-      cp_async_commit();
+      fill(i, slot, i);
       slot = next;
     }
-    int stage = 0, fill = kStages - 1;
-    for (int32_t i = 0; i < take; ++i) {
-      const int32_t next = slot_of(i + kStages);
-      there[kStages - 1] = __ballot_sync(0xffffffffu, slot >= 0);
-      if (i + kStages - 1 < take)
-        S::template issue<true, true>(v, head, slot, ring_u32 + fill * S::kBytes, lane);
-      cp_async_commit();
-      slot = next;
-      fill = fill + 1 == kStages ? 0 : fill + 1;
-      cp_async_wait<kStages - 1>();
-      __syncwarp();
-      const uint8_t* st = ring + stage * S::kBytes;
-      const int32_t t0 = first + i * ws * kStep;
-      // each lane makes one token's numbers ready for all, in place of the four it came with
-      float4* prep = reinterpret_cast<float4*>(ring + stage * S::kBytes + S::kMeta);
-      bool rest;
-      {
-        const float* meta = reinterpret_cast<const float*>(prep);
-        const int32_t zv = __float_as_int(meta[96 + lane]), zc = min(max(zv, -900), 900);
-        const float sk = meta[lane] * (a.scale_log2 * 16777216.0f);
-        const float zk = (static_cast<float>(__float_as_int(meta[32 + lane])) + 8.0f) * -0x1p-24f;
-        const float sv = meta[64 + lane], lv = fminf(fmaxf(__log2f(sv), -40.0f), 40.0f);
-        __syncwarp();
-        prep[lane] = make_float4(sk, zk, lv, sv);
-        prep_z[lane] = __int2half_rn(-1032 - zc);
-        rest = __any_sync(0xffffffffu, zv != zc);
-        if (rest) prep_rest[lane] = static_cast<float>(static_cast<int64_t>(zv) - zc);
-        __syncwarp();
-      }
+
+    // one piece; PLAIN: every row sees every token, and no zero leaves a remainder
+    auto piece = [&](auto plain, uint8_t* st, uint32_t there, int32_t t0, bool force) {
+      constexpr bool PLAIN = decltype(plain)::value;
+      const float4* prep = reinterpret_cast<const float4*>(st + S::kMeta);
       float x[2][NC][4], top[NC][2];
 #pragma unroll
       for (int n = 0; n < NC; ++n) top[n][0] = top[n][1] = -INFINITY;
-      const bool clear = there[0] == 0xffffffffu && t0 + kStep <= all_limit;   // every row sees every token
+      float hi[2][NC][4];
+      key_scores<D, NC>(st, lane, q, x, hi);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float hi[NC][4];
-        key_scores<D, NC>(st, 16 * h, g, c, q, x[h], hi);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {                     // tokens g and g + 8
           const int t = 16 * h + 8 * e + g;
           const float4 k = prep[t];
 #pragma unroll
           for (int n = 0; n < NC; ++n) {
-            float* y = &x[h][n][2 * e];
-            const uint64_t sum = f2_fma(f2_pack(hi[n][2 * e], hi[n][2 * e + 1]), f2_pack(0.0625f, 0.0625f),
-                                        f2_pack(y[0], y[1]));
-            f2_unpack(f2_mul(f2_fma(f2_pack(k.y, k.y), qsum[n], sum), f2_pack(k.x, k.x)), y[0], y[1]);
-            if (!clear) {
-              const bool is = (there[0] >> t) & 1u;
-              if (!(is && t0 + t < limit[n][0])) y[0] = -INFINITY;
-              if (!(is && t0 + t < limit[n][1])) y[1] = -INFINITY;
+            float* y = &x[h][n][2 * e];                   // x_t - m
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              y[i] = fmaf(fmaf(k.y, qsum[n][i], fmaf(hi[h][n][2 * e + i], 0.0625f, y[i])), k.x, nm[n][i]);
+            if constexpr (!PLAIN) {
+              const bool is = (there >> t) & 1u;
+              if (!is || t0 + t >= row_limit[8 * n + 2 * c]) y[0] = -INFINITY;
+              if (!is || t0 + t >= row_limit[8 * n + 2 * c + 1]) y[1] = -INFINITY;
             }
-            float y0, y1;
-            f2_unpack(f2_add(f2_pack(y[0], y[1]), f2_pack(k.z, k.z)), y0, y1);
-            top[n][0] = fmaxf(top[n][0], y0);
-            top[n][1] = fmaxf(top[n][1], y1);
+            top[n][0] = fmaxf(top[n][0], y[0] + k.z);
+            top[n][1] = fmaxf(top[n][1], y[1] + k.z);
           }
         }
       }
-      bool grown = false;
+      float over = top[0][0];
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int s = 4; s < 32; s <<= 1) top[n][k] = fmaxf(top[n][k], __shfl_xor_sync(0xffffffffu, top[n][k], s));
-          grown |= top[n][k] > m[n][k];
-        }
-      if (__any_sync(0xffffffffu, grown)) {
+      for (int n = 0; n < NC; ++n) over = fmaxf(fmaxf(over, top[n][0]), top[n][1]);
+      if (__any_sync(0xffffffffu, over > 8.0f) || force) {
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-          float f[2];
+          float up[2], f[2];                              // what m grows by
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float m1 = fmaxf(m[n][k], top[n][k]);
-            f[k] = m[n][k] == m1 ? 1.0f : exp2_fast(m[n][k] - m1);
-            m[n][k] = m1;
+            float y = top[n][k];
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, s));
+            const uint32_t bit = 1u << (2 * n + k);
+            up[k] = started & bit ? fmaxf(y, 0.0f) : y == -INFINITY ? 0.0f : y;
+            f[k] = started & bit ? exp2_fast(-up[k]) : 1.0f;
+            if (y != -INFINITY) started |= bit;
             zs[n][k] *= f[k];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              x[h][n][k] -= up[k];
+              x[h][n][2 + k] -= up[k];
+            }
           }
+          nm[n][0] -= up[0];
+          nm[n][1] -= up[1];
           const uint64_t f2 = f2_pack(f[0], f[1]);
           l2[n] = f2_mul(l2[n], f2);
 #pragma unroll
@@ -276,10 +266,6 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
           }
         }
       }
-      uint64_t m0[NC];
-#pragma unroll
-      for (int n = 0; n < NC; ++n)
-        m0[n] = f2_pack(m[n][0] == -INFINITY ? 0.0f : -m[n][0], m[n][1] == -INFINITY ? 0.0f : -m[n][1]);
       uint32_t wh[2][NC][2], wl[2][NC][2], z1024[2][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -290,19 +276,20 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
           z1024[h][e] = *reinterpret_cast<const uint32_t*>(prep_z + 16 * h + 8 * e + 2 * c);
 #pragma unroll
           for (int n = 0; n < NC; ++n) {
-            float p0, p1, w0, w1;
-            f2_unpack(f2_add(f2_pack(x[h][n][2 * e], x[h][n][2 * e + 1]), m0[n]), p0, p1);
-            const uint64_t p = f2_pack(exp2_fast(p0), exp2_fast(p1));
-            l2[n] = f2_add(l2[n], p);
-            f2_unpack(f2_mul(p, f2_pack(sv, sv)), w0, w1);
-            if (!clear) {                                  // a scale that is not seen may be anything
-              if (x[h][n][2 * e] == -INFINITY) w0 = 0.0f;
-              if (x[h][n][2 * e + 1] == -INFINITY) w1 = 0.0f;
-            }
-            if (rest) {
+            const float y0 = x[h][n][2 * e], y1 = x[h][n][2 * e + 1];
+            float w0, w1;
+            const float p0 = exp2_fast(y0), p1 = exp2_fast(y1);
+            l2[n] = f2_add(l2[n], f2_pack(p0, p1));
+            w0 = p0 * sv;
+            w1 = p1 * sv;
+            if constexpr (!PLAIN) {
+              if (y0 == -INFINITY) w0 = 0.0f;              // a scale that is not seen may be anything
+              if (y1 == -INFINITY) w1 = 0.0f;
               const float r = prep_rest[t];
-              zs[n][0] = fmaf(w0, r, zs[n][0]);
-              zs[n][1] = fmaf(w1, r, zs[n][1]);
+              if (r != 0.0f) {
+                zs[n][0] = fmaf(w0, r, zs[n][0]);
+                zs[n][1] = fmaf(w1, r, zs[n][1]);
+              }
             }
             const __half2 hi = __floats2half2_rn(w0, w1);
             const float2 back = __half22float2(hi);
@@ -315,16 +302,47 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
         }
       }
       value_products<D, NC>(st + S::kCodes, g, c, z1024, wh, wl, o);
+    };
+
+    int stage = 0;
+    bool force = true;                                   // some column may have seen no key yet
+    for (int32_t i = 0; i < take; ++i) {
+      const int32_t next = slot_of(i + kStages);
+      fill(i + kStages - 1, slot, stage == 0 ? kStages - 1 : stage - 1);
+      slot = next;
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      uint8_t* st = ring + stage * S::kBytes;
+      const int32_t t0 = first + i * ws * kStep;
+      // each lane makes one token's numbers ready for all, in place of the four it came with
+      float4* prep = reinterpret_cast<float4*>(st + S::kMeta);
+      const float* meta = reinterpret_cast<const float*>(prep);
+      const uint32_t there = piece_there[stage];
+      const int32_t zv = __float_as_int(meta[96 + lane]), zc = min(max(zv, -900), 900);
+      const float sk = meta[lane] * (a.scale_log2 * 16777216.0f);
+      const float zk = (static_cast<float>(__float_as_int(meta[32 + lane])) + 8.0f) * -0x1p-24f;
+      const float sv = meta[64 + lane], lv = fminf(fmaxf(__log2f(sv), -40.0f), 40.0f);
+      const bool plain = there == 0xffffffffu && t0 + kStep <= all_limit && !__any_sync(0xffffffffu, zv != zc);
+      __syncwarp();
+      prep[lane] = make_float4(sk, zk, lv, sv);
+      prep_z[lane] = __int2half_rn(-1032 - zc);
+      prep_rest[lane] = static_cast<float>(static_cast<int64_t>(zv) - zc);
+      __syncwarp();
+      if (plain) piece(std::true_type{}, st, there, t0, force);
+      else piece(std::false_type{}, st, there, t0, force);
+      if (force) force = __any_sync(0xffffffffu, started != (1u << (2 * NC)) - 1);
       stage = stage + 1 == kStages ? 0 : stage + 1;
-#pragma unroll
-      for (int s = 0; s + 1 < kStages; ++s) there[s] = there[s + 1];
       __syncwarp();
     }
     cp_async_wait<0>();
 
-    float l[NC][2];
+    float m[NC][2], l[NC][2];
 #pragma unroll
-    for (int n = 0; n < NC; ++n) f2_unpack(l2[n], l[n][0], l[n][1]);
+    for (int n = 0; n < NC; ++n) {
+      f2_unpack(l2[n], l[n][0], l[n][1]);
+      m[n][0] = -nm[n][0];
+      m[n][1] = -nm[n][1];
+    }
     // sums of column k of product j, row g or g + 8, without the remainder
     auto sum_of = [&](int j, int n, int k, bool upper) {
       float y[2];
@@ -340,15 +358,14 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
           l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], s);
           zs[n][k] += __shfl_xor_sync(0xffffffffu, zs[n][k], s);
         }
-    const bool whole = take == tu;
-    const int part = at == start ? 0 : 1;
+    const int part = done == 0 ? 0 : 1;
     if (ws == 1) {
 #pragma unroll
       for (int n = 0; n < NC; ++n)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          if (!has[n][k]) continue;
           const int32_t r = 8 * n + 2 * c + k, rr = row0 + r;
+          if (rr >= all_rows) continue;
           const float inv = whole ? inverse_or_zero(l[n][k]) : 1.0f;
           float y[T::kPer];
 #pragma unroll
@@ -418,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
       }
       __syncthreads();
     }
-    at += take;
+    done += take;
   }
 }
 

@@ -71,13 +71,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
-               : "memory");
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0)
-               : "memory");
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -92,8 +90,9 @@ struct KvStage {
   static constexpr int kCodes = 32 * kRow;
   static constexpr int kMeta = 2 * kCodes;
   static constexpr int kBytes = 2 * kCodes + 4 * 32 * 4;
-  // what a warp makes of the numbers besides, one piece at a time: a remainder and a half a token
-  static constexpr int kPrepared = 32 * 4 + 32 * 2;
+  // what a warp keeps besides: a remainder and a half a token of the piece at hand, the tokens that are there
+  // of every piece, the rows' limits
+  static constexpr int kPrepared = 32 * 4 + 32 * 2 + 4 * 4 + 16 * 4;
 
   // Key row of token t: a lane of column c of the fragment reads chunk c (and c + 4 when D = 256;
   // less than a chunk when D < 128) of rows g and g + 8.  Only D = 256 needs a swizzle: its
@@ -112,61 +111,59 @@ struct KvStage {
     return row * kRow + (x << 4);
   }
 
-  // Starts the copy of 32 tokens; lane t knows its token's slot (negative: none, zeros are stored).
+  // Starts the copy of 32 tokens; lane t knows its token's slot (any slot for a token that is not there).
+  // key, value: where chunk lane % kChunks of the head stands in a row; j: the head's group.  (A cache
+  // has less than 2^32 groups.)
   template <bool KEYS, bool VALUES>
-  __device__ static __forceinline__ void issue(const KvView& v, int head, int32_t slot, uint32_t smem,
-                                               int lane) {
+  __device__ static __forceinline__ void issue(const KvView& v, const uint8_t* key, const uint8_t* value,
+                                               uint32_t j, uint32_t slot, uint32_t smem, int lane) {
     constexpr int kPer = 32 / kChunks;                  // tokens of one round of copies
-    const int64_t row_bytes = v.width >> 1;
-    const int at = head * kRow;
+    const uint32_t row_bytes = static_cast<uint32_t>(v.width) >> 1;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int t = i * kPer + lane / kChunks, chunk = lane % kChunks;
-      const int32_t s = __shfl_sync(0xffffffffu, slot, t);
-      const int64_t off = max(s, 0) * row_bytes + at + chunk * 16;
-      if (KEYS) cp_async_16(smem + key_at(t, chunk), v.codes[0] + off, s >= 0);
-      if (VALUES) cp_async_16(smem + kCodes + value_at(value_row(t), chunk), v.codes[1] + off, s >= 0);
+      const uint64_t off = static_cast<uint64_t>(__shfl_sync(0xffffffffu, slot, t)) * row_bytes;
+      if (KEYS) cp_async_16(smem + key_at(t, chunk), key + off);
+      if (VALUES) cp_async_16(smem + kCodes + value_at(value_row(t), chunk), value + off);
     }
-    const int64_t m = static_cast<int64_t>(max(slot, 0)) * v.groups + head * D / v.group;
+    const uint32_t m = slot * static_cast<uint32_t>(v.groups) + j;
     if (KEYS) {
-      cp_async_4(smem + kMeta + lane * 4, v.scales[0] + m, slot >= 0);
-      cp_async_4(smem + kMeta + 128 + lane * 4, v.zeros[0] + m, slot >= 0);
+      cp_async_4(smem + kMeta + lane * 4, v.scales[0] + m);
+      cp_async_4(smem + kMeta + 128 + lane * 4, v.zeros[0] + m);
     }
     if (VALUES) {
-      cp_async_4(smem + kMeta + 256 + lane * 4, v.scales[1] + m, slot >= 0);
-      cp_async_4(smem + kMeta + 384 + lane * 4, v.zeros[1] + m, slot >= 0);
+      cp_async_4(smem + kMeta + 256 + lane * 4, v.scales[1] + m);
+      cp_async_4(smem + kMeta + 384 + lane * 4, v.zeros[1] + m);
     }
   }
 };
 
-// Queries as the B operand: lane 4 r + c holds, of query row r, the elements that column c's key words
-// hold: word w covers 8 elements from first(w); pairs (e0, e4), (e2, e6) meet the low nibbles, (e1,
-// e5), (e3, e7) the high ones.
+// Queries as the B operand, in shared memory: lane 4 r + c owns, of query row r, the elements that column
+// c's key words hold: word w covers 8 elements from first(w); pairs (e0, e4), (e2, e6) meet the low
+// nibbles, (e1, e5), (e3, e7) the high ones.
 template <int D>
 struct QueryFrag {
   static constexpr int kWords = D / 32;
-  uint32_t r[kWords][4];
+  static constexpr int kBytes = kWords * 32 * 16;       // of 8 rows: [word][lane] of 16 bytes
 
   __device__ static __forceinline__ int first(int c, int w) {
     return D == 256 ? (w >> 2) * 128 + c * 32 + (w & 3) * 8 : c * (D / 4) + w * 8;
   }
   // row: the query's elements, or null (zeros).  Returns the sum of the lane's elements.
-  __device__ __forceinline__ float load(const __half* row, int c) {
+  __device__ static __forceinline__ float put(uint4* frag, const __half* row, int lane) {
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
       uint4 x = make_uint4(0, 0, 0, 0);
-      if (row != nullptr) x = *reinterpret_cast<const uint4*>(row + first(c, w));
+      if (row != nullptr) x = *reinterpret_cast<const uint4*>(row + first(lane & 3, w));
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&x);        // (e0 e1) (e2 e3) (e4 e5) (e6 e7)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(p + i));
         sum += f.x + f.y;
       }
-      r[w][0] = byte_perm(x.x, x.z, 0x5410);
-      r[w][1] = byte_perm(x.y, x.w, 0x5410);
-      r[w][2] = byte_perm(x.x, x.z, 0x7632);
-      r[w][3] = byte_perm(x.y, x.w, 0x7632);
+      frag[w * 32 + lane] = make_uint4(byte_perm(x.x, x.z, 0x5410), byte_perm(x.y, x.w, 0x5410),
+                                       byte_perm(x.x, x.z, 0x7632), byte_perm(x.y, x.w, 0x7632));
     }
     return sum;
   }
@@ -194,28 +191,37 @@ __device__ __forceinline__ void load_key_words(const uint8_t* keys, int t, int c
   }
 }
 
-// Sums over the low and the high nibbles, 2^-24 and 2^-20 sum q u, for 16 tokens (rows t0 + g and t0 + g
-// + 8) and 8 NC queries.
+// Sums over the low and the high nibbles, 2^-24 and 2^-20 sum q u, for 32 tokens (rows 16 h + g and 16 h +
+// g + 8) and 8 NC queries.
 template <int D, int NC>
-__device__ __forceinline__ void key_scores(const uint8_t* keys, int t0, int g, int c,
-                                           const QueryFrag<D> (&q)[NC], float (&lo)[NC][4],
-                                           float (&hi)[NC][4]) {
-  uint32_t xa[D / 32], xb[D / 32];
-  load_key_words<D>(keys, t0 + g, c, xa);
-  load_key_words<D>(keys, t0 + g + 8, c, xb);
+__device__ __forceinline__ void key_scores(const uint8_t* keys, int lane, const uint4* q, float (&lo)[2][NC][4],
+                                           float (&hi)[2][NC][4]) {
+  const int g = lane >> 2, c = lane & 3;
+  uint32_t x[2][2][D / 32];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    load_key_words<D>(keys, 16 * h + g, c, x[h][0]);
+    load_key_words<D>(keys, 16 * h + g + 8, c, x[h][1]);
+  }
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) {
-    const uint32_t ya = xa[w] >> 8, yb = xb[w] >> 8;
-    const uint32_t l0 = nib_low(xa[w]), l1 = nib_low(xb[w]), l2 = nib_low(ya), l3 = nib_low(yb);
-    const uint32_t h0 = nib_high(xa[w]), h1 = nib_high(xb[w]), h2 = nib_high(ya), h3 = nib_high(yb);
+    uint4 b[NC];
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      if (w == 0) {
-        mma_16x8x16_first(lo[n], l0, l1, l2, l3, q[n].r[w][0], q[n].r[w][1]);
-        mma_16x8x16_first(hi[n], h0, h1, h2, h3, q[n].r[w][2], q[n].r[w][3]);
-      } else {
-        mma_16x8x16(lo[n], l0, l1, l2, l3, q[n].r[w][0], q[n].r[w][1]);
-        mma_16x8x16(hi[n], h0, h1, h2, h3, q[n].r[w][2], q[n].r[w][3]);
+    for (int n = 0; n < NC; ++n) b[n] = q[(n * (D / 32) + w) * 32 + lane];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t xa = x[h][0][w], xb = x[h][1][w], ya = xa >> 8, yb = xb >> 8;
+      const uint32_t l0 = nib_low(xa), l1 = nib_low(xb), l2 = nib_low(ya), l3 = nib_low(yb);
+      const uint32_t h0 = nib_high(xa), h1 = nib_high(xb), h2 = nib_high(ya), h3 = nib_high(yb);
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        if (w == 0) {
+          mma_16x8x16_first(lo[h][n], l0, l1, l2, l3, b[n].x, b[n].y);
+          mma_16x8x16_first(hi[h][n], h0, h1, h2, h3, b[n].z, b[n].w);
+        } else {
+          mma_16x8x16(lo[h][n], l0, l1, l2, l3, b[n].x, b[n].y);
+          mma_16x8x16(hi[h][n], h0, h1, h2, h3, b[n].z, b[n].w);
+        }
       }
     }
   }

@@ -29,6 +29,10 @@ qr_status make_view(const qr_kv_cache* c, const qr_kv_seqs* s, int64_t tokens, b
   if (width > 65536 || s->batch > 4096 || tokens > (1 << 30)) return QR_ERR_UNSUPPORTED;
   const int64_t capacity = static_cast<int64_t>(s->max_pages) * c->page_size;
   if (capacity >= (1 << 30) || c->slots / c->page_size > 0x7FFFFFFF) return QR_ERR_UNSUPPORTED;
+  // slots and pages of the batch are counted in 32 bits, groups of the cache in unsigned ones
+  if (c->slots > 0x7FFFFFFF || static_cast<int64_t>(s->batch) * s->max_pages > 0x7FFFFFFF ||
+      c->slots * (width / c->group) > 0xFFFFFFFFll)
+    return QR_ERR_UNSUPPORTED;
   if (c->slots > 0) {
     if (!c->k_codes || !c->k_scales || !c->k_zeros || !c->v_codes || !c->v_scales || !c->v_zeros)
       return QR_ERR_INVALID_ARG;
@@ -58,7 +62,7 @@ qr_status make_view(const qr_kv_cache* c, const qr_kv_seqs* s, int64_t tokens, b
   v->page_magic = static_cast<uint32_t>(
       ((uint64_t(1) << 32) * ((uint64_t(1) << l) - c->page_size)) / c->page_size + 1);
   v->max_pages = s->max_pages;
-  v->capacity = static_cast<int32_t>(capacity);
+  v->capacity = v->pages > 0 ? static_cast<int32_t>(capacity) : 0;   // no pages: nothing is held
   v->batch = s->batch;
   v->heads = c->heads;
   v->head_dim = d;
