@@ -111,12 +111,12 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
   const int64_t units = prefix[v.batch];
   if (blockIdx.x == 0)
     for (int32_t b = threadIdx.x; b <= v.batch; b += kThreads) a.prefix[b] = prefix[b];
-  // this block's units, from the start of its range (a range has less than 2^31)
-  const int32_t count = static_cast<int32_t>(range_start(a.plan, units, blockIdx.x + 1) -
-                                             range_start(a.plan, units, blockIdx.x));
+  const Ranges ranges = Ranges::of(a.plan, units);
+  const int64_t start = ranges.start(blockIdx.x);
+  const int32_t count = ranges.count(blockIdx.x);
   int32_t b = 0;
   for (int32_t done = 0; done < count;) {
-    const int64_t at = range_start(a.plan, units, blockIdx.x) + done;
+    const int64_t at = start + done;
     // the item that unit `at` belongs to
     {
       int32_t lo = b, hi = v.batch - 1;                 // the last b with prefix[b] <= at
@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
       off -= static_cast<int64_t>(tu) * a.plan.head_blocks;
       tu = tile_units(a.plan, rows, ++tile);
     }
-    const int32_t block = static_cast<int32_t>(off / tu), u0 = static_cast<int32_t>(off % tu);
+    const int32_t block = a.plan.head_blocks == 1 ? 0 : static_cast<int32_t>(off / tu);
+    const int32_t u0 = static_cast<int32_t>(off - static_cast<int64_t>(block) * tu);
     const int32_t take = min(tu - u0, count - done);
     const bool whole = take == tu;
     const int head = (block << a.heads_log2) + hw;
@@ -458,13 +459,14 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
   if (work) b = kv_seq_of_row(v, i);
   work = work && b < v.batch;
   int32_t first = 0, last = 0, r = 0, hb = 0;
-  int64_t u0 = 0, units = 0;
+  int64_t u0 = 0;
+  Ranges ranges{};
   if (work) {
     const SeqRows rows = seq_rows(v, b);
     const int32_t ti = i - rows.first;
     work = ti >= 0 && ti < rows.here;
     if (work) {
-      units = a.prefix[v.batch];
+      const int64_t units = a.prefix[v.batch];
       const int hk = h / a.plan.gq;
       const int64_t row = static_cast<int64_t>(ti) * a.plan.gq + h % a.plan.gq;
       const int32_t tile = static_cast<int32_t>(row / a.plan.rows);
@@ -474,8 +476,9 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
       for (int32_t t = 0; t < tile; ++t) u0 += static_cast<int64_t>(tile_units(a.plan, rows, t)) * a.plan.head_blocks;
       const int32_t tu = tile_units(a.plan, rows, tile);
       u0 += static_cast<int64_t>(hk >> a.heads_log2) * tu;
-      first = max(range_of(a.plan, units, u0), 0);
-      last = min(range_of(a.plan, units, u0 + tu - 1), a.plan.blocks - 1);
+      ranges = Ranges::of(a.plan, units);
+      first = max(ranges.holder(u0), 0);
+      last = min(ranges.holder(u0 + tu - 1), ranges.blocks - 1);
       work = first < last;
     }
   }
@@ -490,11 +493,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
       int64_t p = 0;
       float2 x = make_float2(-INFINITY, 0.0f);
       if (blk <= last) {
-        const int64_t s = range_start(a.plan, units, blk);
-        if (s < range_start(a.plan, units, blk + 1)) {
-          p = part_at(a, blk, s >= u0 ? 0 : 1, hb, r);
-          x = a.part_ml[p];
-        }
+        p = part_at(a, blk, ranges.start(blk) >= u0 ? 0 : 1, hb, r);
+        x = a.part_ml[p];
       }
       float top = x.x;
 #pragma unroll
@@ -583,10 +583,10 @@ cudaError_t run_split(const SplitArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv_split_kernel<D, NC>, dim3(a.plan.blocks), dim3(kThreads), smem, stream, 1, a);
   if (e != cudaSuccess) return e;
-  // few rows share many parts: eight warps a row, else one
+  // rows of few sequences have many parts, and there are few of them: eight warps a row; else one
   const int64_t rows = static_cast<int64_t>(a.v.tokens) * a.q_heads;
   const int64_t items = std::max<int64_t>(1, static_cast<int64_t>(a.v.batch) * a.plan.head_blocks);
-  return a.plan.blocks > 4 * items
+  return rows <= 8 * sm_count() && a.plan.blocks > 8 * items
              ? launch_pdl(kv_join_kernel<D, 8>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, stream, 1, a)
              : launch_pdl(kv_join_kernel<D, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream,
                           1, a);

@@ -92,12 +92,41 @@ __device__ __forceinline__ void split_prefix(const KvView& v, const SplitPlan& p
   }
 }
 
-__device__ __forceinline__ int64_t range_start(const SplitPlan& p, int64_t units, int32_t block) {
-  return units * block / p.blocks;
-}
-// The block whose range holds unit u.
-__device__ __forceinline__ int32_t range_of(const SplitPlan& p, int64_t units, int64_t u) {
-  return static_cast<int32_t>(((u + 1) * p.blocks - 1) / units);
-}
+// The ranges: `blocks` of them at most, of no fewer than kLeastUnits units while there are several; the first
+// `longer` have one unit more.
+constexpr int32_t kLeastUnits = 2;
+struct Ranges {
+  int32_t blocks, each, longer;
+
+  __device__ static __forceinline__ Ranges of(const SplitPlan& p, int64_t units) {
+    Ranges r;
+    if (units < 0x7FFFFFFF) {                             // (32-bit divisions are several times shorter)
+      const uint32_t u = static_cast<uint32_t>(units);
+      r.blocks = min(max(static_cast<int32_t>(u / kLeastUnits), 1), p.blocks);
+      r.each = static_cast<int32_t>(u / static_cast<uint32_t>(r.blocks));
+      r.longer = static_cast<int32_t>(u - static_cast<uint32_t>(r.blocks) * r.each);
+    } else {
+      r.blocks = p.blocks;
+      r.each = static_cast<int32_t>(units / r.blocks);
+      r.longer = static_cast<int32_t>(units % r.blocks);
+    }
+    return r;
+  }
+  __device__ __forceinline__ int64_t start(int32_t block) const {
+    return static_cast<int64_t>(each) * block + min(block, longer);
+  }
+  __device__ __forceinline__ int32_t count(int32_t block) const {
+    return block >= blocks ? 0 : each + (block < longer ? 1 : 0);
+  }
+  // the range that holds unit u
+  __device__ __forceinline__ int32_t holder(int64_t u) const {
+    const int64_t cut = static_cast<int64_t>(each + 1) * longer;
+    const int64_t x = u < cut ? u : u - cut;
+    const int32_t div = u < cut ? each + 1 : each;
+    const int32_t q = x < 0x7FFFFFFF ? static_cast<int32_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(div))
+                                     : static_cast<int32_t>(x / div);
+    return u < cut ? q : longer + q;
+  }
+};
 
 }  // namespace qr
