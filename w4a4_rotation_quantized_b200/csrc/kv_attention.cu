@@ -48,7 +48,7 @@ struct SplitArgs {
   __half* out;
   int64_t ldo;
   float* lse;
-  int64_t* prefix;                             // [batch + 1]
+  int64_t* prefix;                             // [batch + 1]; null: no item is cut
   float2* part_ml;                             // [2 blocks][heads of a block][rows]
   float* part_o;                               // ... [D]
   int32_t heads_log2;                          // heads of a block = 2^heads_log2
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
   grid_dep_launch();
   split_prefix<kThreads>(v, a.plan, prefix);
   const int64_t units = prefix[v.batch];
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0 && a.prefix != nullptr)
     for (int32_t b = threadIdx.x; b <= v.batch; b += kThreads) a.prefix[b] = prefix[b];
   const Ranges ranges = Ranges::of(a.plan, units);
   const int64_t start = ranges.start(blockIdx.x);
@@ -173,8 +173,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
     }
     uint32_t started = 0;                                // bit 2 n + k: the column has seen a key
 
-    // this warp's pieces: tokens first + 32 ws i
-    const int32_t first = (u0 * ws + sw) * kStep;
+    // this warp's pieces: 32 tokens from first + 32 ws i
+    const int32_t first = u0 * a.plan.unit + sw * kStep;
+    const int32_t pieces = min(take * (a.plan.unit / (ws * kStep)),
+                               (max(n_seen - u0 * a.plan.unit, 0) + ws * kStep - 1) / (ws * kStep));
     const uint8_t* key = v.codes[0] + head * S::kRow + lane % S::kChunks * 16;
     const uint8_t* value = v.codes[1] + head * S::kRow + lane % S::kChunks * 16;
     const uint32_t group = head * D / v.group;
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
     auto fill = [&](int32_t i, int32_t slot, int stage) {
       const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
       if (lane == 0) piece_there[stage] = there;
-      if (i < take) S::template issue<true, true>(v, key, value, group, max(slot, 0), ring_u32 + stage * S::kBytes, lane);
+      if (i < pieces) S::template issue<true, true>(v, key, value, group, max(slot, 0), ring_u32 + stage * S::kBytes, lane);
       cp_async_commit();
     };
     int32_t slot = slot_of(0);
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
 
     int stage = 0;
     bool force = true;                                   // some column may have seen no key yet
-    for (int32_t i = 0; i < take; ++i) {
+    for (int32_t i = 0; i < pieces; ++i) {
       const int32_t next = slot_of(i + kStages);
       fill(i + kStages - 1, slot, stage == 0 ? kStages - 1 : stage - 1);
       slot = next;
@@ -440,19 +442,23 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
   }
 }
 
-// Adds up the parts of the rows whose items were cut.  One group of JW warps a (token, query head): its
-// warps take every JW-th part, lanes the elements of the head.
+// Adds up the parts of the rows whose items were cut.  JW = 1: one warp a (token, query head), its lanes the
+// elements of the head.  JW = 8, for few rows with many parts: one block a (token, query head, 32 elements),
+// its warps take every eighth part.
 template <int D, int JW>
 __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
-  constexpr int E = D / 32;
+  constexpr int E = JW == 1 ? D / 32 : 1;
   constexpr int kGroups = 8 / JW;
-  __shared__ float acc[kGroups][JW > 1 ? JW : 1][D];
-  __shared__ float2 ml[kGroups][JW > 1 ? JW : 1];
+  constexpr int kSlices = JW == 1 ? 1 : D / 32;
+  constexpr int F = JW == 1 ? 8 : 16;                    // parts in flight
+  __shared__ float acc[JW][32];
+  __shared__ float2 ml[JW];
   const KvView& v = a.v;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp / JW, jw = warp % JW;
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t job = static_cast<int64_t>(blockIdx.x) * kGroups + grp;
+  const int64_t job = static_cast<int64_t>(blockIdx.x / kSlices) * kGroups + grp;
+  const int e0 = blockIdx.x % kSlices * 32 + lane;       // this lane's elements: e0 + 32 e
   const int32_t i = static_cast<int32_t>(job / a.q_heads), h = static_cast<int32_t>(job % a.q_heads);
   bool work = i < v.tokens;
   int32_t b = v.batch;
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
   if (work) {
-    // 32 parts at a time: their m and l, one a lane, then their sums, eight in flight
+    // 32 parts at a time: their m and l, one a lane, then their sums, several in flight
     for (int32_t c0 = first; c0 <= last; c0 += 32 * JW) {
       const int32_t blk = c0 + lane * JW + jw;
       int64_t p = 0;
@@ -513,61 +519,75 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
       for (int e = 0; e < E; ++e) o[e] *= keep;
       uint32_t left = __ballot_sync(0xffffffffu, x.y != 0.0f);
       while (left != 0) {
-        float f8[8], y[8][E];
+        float f8[F], y[F][E];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < F; ++k) {
           const int from = left != 0 ? __ffs(left) - 1 : -1;
           left &= left - 1;
           const int64_t pk = __shfl_sync(0xffffffffu, p, max(from, 0));
           f8[k] = __shfl_sync(0xffffffffu, mine, max(from, 0));
           const float* src = a.part_o + pk * D;
 #pragma unroll
-          for (int e = 0; e < E; ++e) y[k][e] = from >= 0 ? src[e * 32 + lane] : 0.0f;
+          for (int e = 0; e < E; ++e) y[k][e] = from >= 0 ? src[e0 + 32 * e] : 0.0f;
           if (from < 0) f8[k] = 0.0f;
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < F; ++k)
 #pragma unroll
           for (int e = 0; e < E; ++e) o[e] = fmaf(y[k][e], f8[k], o[e]);
       }
     }
   }
   if (JW > 1) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[grp][jw][e * 32 + lane] = o[e];
-    if (lane == 0) ml[grp][jw] = make_float2(m, l);
+    acc[jw][lane] = o[0];
+    if (lane == 0) ml[jw] = make_float2(m, l);
     __syncthreads();
     if (!work || jw != 0) return;
-    for (int w = 0; w < JW; ++w) m = fmaxf(m, ml[grp][w].x);
-    l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int w = 0; w < JW; ++w) m = fmaxf(m, ml[w].x);
+    l = o[0] = 0.0f;
     for (int w = 0; w < JW; ++w) {
-      const float2 x = ml[grp][w];
+      const float2 x = ml[w];
       const float f = x.y == 0.0f ? 0.0f : x.x == m ? 1.0f : exp2_fast(x.x - m);
       l = fmaf(x.y, f, l);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(acc[grp][w][e * 32 + lane], f, o[e]);
+      o[0] = fmaf(acc[w][lane], f, o[0]);
     }
   }
   const float inv = inverse_or_zero(l);
 #pragma unroll
-  for (int e = 0; e < E; ++e) a.out[i * a.ldo + h * D + e * 32 + lane] = __float2half_rn(o[e] * inv);
-  if (a.lse != nullptr && lane == 0) a.lse[static_cast<int64_t>(i) * a.q_heads + h] = row_lse(m, l);
+  for (int e = 0; e < E; ++e) a.out[i * a.ldo + h * D + e0 + 32 * e] = __float2half_rn(o[e] * inv);
+  if (a.lse != nullptr && e0 == 0) a.lse[static_cast<int64_t>(i) * a.q_heads + h] = row_lse(m, l);
 }
 
 struct SplitSizes {
-  int nc, heads_log2, blocks;
+  int nc, heads_log2, blocks, unit;
+  bool whole;                                  // no item is cut: nothing to join
   int64_t prefix_bytes, ml_bytes, bytes;
 };
+
+// Short contexts on few heads: fewer heads a block, more warps a head (they join in shared memory), and items
+// that are not cut, which spares the second kernel; taken where all items fit one wave of blocks with at
+// most kWholePieces pieces a warp.  Elsewhere eight heads a block: warps that read the same tokens' scales
+// share their sectors (one head a block: 64 us instead of 58 for one sequence of 131072 tokens, 64/8 heads).
+constexpr int kWholePieces = 8;
 
 SplitSizes split_sizes(const KvView& v, int32_t q_heads) {
   SplitSizes s{};
   const int gq = q_heads / v.heads;
   const int64_t rows = (static_cast<int64_t>(v.tokens) * gq + v.batch - 1) / v.batch;   // of a sequence, on average
   s.nc = rows > 8 && v.head_dim <= 128 ? 2 : 1;
-  while (s.heads_log2 < 3 && v.heads % (2 << s.heads_log2) == 0) ++s.heads_log2;
   s.blocks = sm_count() * (v.head_dim == 256 || s.nc == 2 ? 1 : 2);
+  int most = 0;
+  while (most < 3 && v.heads % (2 << most) == 0) ++most;
+  const int64_t tiles = std::max<int64_t>(v.batch, (static_cast<int64_t>(v.tokens) * gq + 8 * s.nc - 1) / (8 * s.nc));
+  while (s.heads_log2 < most && tiles * (v.heads >> s.heads_log2) > s.blocks) ++s.heads_log2;
+  int step = kStep * (kWarps >> s.heads_log2);
+  s.whole = tiles * (v.heads >> s.heads_log2) <= s.blocks && v.capacity <= kWholePieces * step;
+  if (!s.whole) {
+    s.heads_log2 = most;
+    step = kStep * (kWarps >> most);
+  }
+  s.unit = s.whole ? kWholePieces * step : step;
+  if (s.whole) return s;
   s.prefix_bytes = (8 * (static_cast<int64_t>(v.batch) + 1) + 255) / 256 * 256;
   const int64_t parts = (2ll * s.blocks << s.heads_log2) * 8 * s.nc;
   s.ml_bytes = parts * 8;
@@ -582,12 +602,12 @@ cudaError_t run_split(const SplitArgs& a, cudaStream_t stream) {
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv_split_kernel<D, NC>, dim3(a.plan.blocks), dim3(kThreads), smem, stream, 1, a);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.prefix == nullptr) return e;
   // rows of few sequences have many parts, and there are few of them: eight warps a row; else one
   const int64_t rows = static_cast<int64_t>(a.v.tokens) * a.q_heads;
   const int64_t items = std::max<int64_t>(1, static_cast<int64_t>(a.v.batch) * a.plan.head_blocks);
   return rows <= 8 * sm_count() && a.plan.blocks > 8 * items
-             ? launch_pdl(kv_join_kernel<D, 8>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, stream, 1, a)
+             ? launch_pdl(kv_join_kernel<D, 8>, dim3(static_cast<unsigned>(rows * (D / 32))), dim3(256), 0, stream, 1, a)
              : launch_pdl(kv_join_kernel<D, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream,
                           1, a);
 }
@@ -602,7 +622,7 @@ qr_status launch_kv_attention(const KvView& v, const KvAttentionJob& j, cudaStre
   a.v = v;
   a.plan.gq = j.q_heads / v.heads;
   a.plan.rows = 8 * s.nc;
-  a.plan.unit = kStep * (kWarps >> s.heads_log2);
+  a.plan.unit = s.unit;
   a.plan.head_blocks = v.heads >> s.heads_log2;
   a.plan.blocks = s.blocks;
   a.plan.causal = j.causal;
@@ -613,7 +633,7 @@ qr_status launch_kv_attention(const KvView& v, const KvAttentionJob& j, cudaStre
   a.out = reinterpret_cast<__half*>(j.out);
   a.ldo = j.ldo;
   a.lse = j.lse;
-  a.prefix = static_cast<int64_t*>(j.workspace);
+  a.prefix = s.whole ? nullptr : static_cast<int64_t*>(j.workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(j.workspace) + s.prefix_bytes);
   a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(j.workspace) + s.prefix_bytes + s.ml_bytes);
   a.heads_log2 = s.heads_log2;

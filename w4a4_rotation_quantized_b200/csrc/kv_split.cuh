@@ -92,9 +92,9 @@ __device__ __forceinline__ void split_prefix(const KvView& v, const SplitPlan& p
   }
 }
 
-// The ranges: `blocks` of them at most, of no fewer than kLeastUnits units while there are several; the first
+// The ranges: `blocks` of them at most, of no fewer than kLeastUnits units; the first
 // `longer` have one unit more.
-constexpr int32_t kLeastUnits = 2;
+constexpr int32_t kLeastUnits = 1;
 struct Ranges {
   int32_t blocks, each, longer;
 
