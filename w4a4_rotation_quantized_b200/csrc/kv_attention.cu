@@ -24,7 +24,7 @@
 #include <type_traits>
 
 #include "kv_mma.cuh"
-#include "kv_split.cuh"
+#include "kv_split_args.cuh"
 #include "qr_internal.h"
 
 namespace qr {
@@ -37,46 +37,6 @@ constexpr int kThreads = 32 * kWarps;
 template <int D>
 constexpr int stages() { return 2; }
 constexpr int kStep = 32;                      // tokens of a piece
-
-struct SplitArgs {
-  KvView v;
-  SplitPlan plan;
-  const __half* q;
-  int64_t ldq;
-  int32_t q_heads;
-  float scale_log2;                            // scale * log2 e
-  __half* out;
-  int64_t ldo;
-  float* lse;
-  int64_t* prefix;                             // [batch + 1]; null: no item is cut
-  float2* part_ml;                             // [2 blocks][heads of a block][rows]
-  float* part_o;                               // ... [D]
-  int32_t heads_log2;                          // heads of a block = 2^heads_log2
-};
-
-// A part's place: slot 0 holds the part that begins a block's range, slot 1 one that ends it.
-__device__ __forceinline__ int64_t part_at(const SplitArgs& a, int32_t block, int slot, int head, int row) {
-  return (((static_cast<int64_t>(block) * 2 + slot) << a.heads_log2) + head) * a.plan.rows + row;
-}
-
-// Writes N fp16 values of a finished row.
-template <int N>
-__device__ __forceinline__ void store_half(__half* to, const float (&x)[N]) {
-  __half2 h[N / 2];
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-  if constexpr (N >= 8) {
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(h)[i];
-  } else {
-    *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(h);
-  }
-}
-
-__device__ __forceinline__ float row_lse(float m, float l) {
-  return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-}
-__device__ __forceinline__ float inverse_or_zero(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
 template <int D, int NC>
 constexpr int ring_bytes() { return kWarps * (stages<D>() * KvStage<D>::kBytes + KvStage<D>::kPrepared + NC * QueryFrag<D>::kBytes); }
@@ -117,28 +77,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
   int32_t b = 0;
   for (int32_t done = 0; done < count;) {
     const int64_t at = start + done;
-    // the item that unit `at` belongs to
-    {
-      int32_t lo = b, hi = v.batch - 1;                 // the last b with prefix[b] <= at
-      while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= at) lo = mid; else hi = mid - 1;
-      }
-      b = lo;
-    }
-    const SeqRows rows = seq_rows(v, b);
-    int64_t off = at - prefix[b];
-    int32_t tile = 0, tu = tile_units(a.plan, rows, 0);
-    while (off >= static_cast<int64_t>(tu) * a.plan.head_blocks) {
-      off -= static_cast<int64_t>(tu) * a.plan.head_blocks;
-      tu = tile_units(a.plan, rows, ++tile);
-    }
-    const int32_t block = a.plan.head_blocks == 1 ? 0 : static_cast<int32_t>(off / tu);
-    const int32_t u0 = static_cast<int32_t>(off - static_cast<int64_t>(block) * tu);
-    const int32_t take = min(tu - u0, count - done);
-    const bool whole = take == tu;
+    const Item it = find_item(v, a.plan, prefix, at, count - done, &b);
+    const SeqRows& rows = it.rows;
+    const int32_t tile = it.tile, block = it.block, u0 = it.unit, take = it.take, n_seen = it.seen;
+    const bool whole = it.whole;
     const int head = (block << a.heads_log2) + hw;
-    const int32_t n_seen = tile_seen(a.plan, rows, tile);
 
     // queries of this tile: row r is new token r / gq, head r % gq of the group
     const int32_t row0 = tile * R, all_rows = rows.here * a.plan.gq;
@@ -442,53 +385,74 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
   }
 }
 
-// Adds up the parts of the rows whose items were cut.  JW = 1: one warp a (token, query head), its lanes the
-// elements of the head.  JW = 8, for few rows with many parts: one block a (token, query head, 32 elements),
-// its warps take every eighth part.
+// Adds up the parts of items that were cut.  JW = 1: one warp a row, its lanes the elements of the head; a block
+// looks after the item that range blockIdx.y is the first to hold and not the last, if there is one, and
+// takes eight of its rows (token, query head).  JW = 8, for few rows with many parts: one block a row and 32
+// elements, its warps take every eighth part.
 template <int D, int JW>
 __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
   constexpr int E = JW == 1 ? D / 32 : 1;
-  constexpr int kGroups = 8 / JW;
-  constexpr int kSlices = JW == 1 ? 1 : D / 32;
   constexpr int F = JW == 1 ? 8 : 16;                    // parts in flight
   __shared__ float acc[JW][32];
   __shared__ float2 ml[JW];
   const KvView& v = a.v;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp / JW, jw = warp % JW;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, jw = JW == 1 ? 0 : warp;
+  const int e0 = JW == 1 ? lane : blockIdx.x % (D / 32) * 32 + lane;       // this lane's elements: e0 + 32 e
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t job = static_cast<int64_t>(blockIdx.x / kSlices) * kGroups + grp;
-  const int e0 = blockIdx.x % kSlices * 32 + lane;       // this lane's elements: e0 + 32 e
-  const int32_t i = static_cast<int32_t>(job / a.q_heads), h = static_cast<int32_t>(job % a.q_heads);
-  bool work = i < v.tokens;
-  int32_t b = v.batch;
-  if (work) b = kv_seq_of_row(v, i);
-  work = work && b < v.batch;
-  int32_t first = 0, last = 0, r = 0, hb = 0;
+  const int64_t units = a.prefix[v.batch];
+  const Ranges ranges = Ranges::of(a.plan, units);
+  bool work = false;
+  int32_t i = 0, h = 0, first = 0, last = 0, r = 0, hb = 0;   // row, query head, ranges that hold the item, place
   int64_t u0 = 0;
-  Ranges ranges{};
-  if (work) {
-    const SeqRows rows = seq_rows(v, b);
-    const int32_t ti = i - rows.first;
-    work = ti >= 0 && ti < rows.here;
-    if (work) {
-      const int64_t units = a.prefix[v.batch];
-      const int hk = h / a.plan.gq;
-      const int64_t row = static_cast<int64_t>(ti) * a.plan.gq + h % a.plan.gq;
-      const int32_t tile = static_cast<int32_t>(row / a.plan.rows);
-      r = static_cast<int32_t>(row % a.plan.rows);
-      hb = hk & ((1 << a.heads_log2) - 1);
-      u0 = a.prefix[b];
-      for (int32_t t = 0; t < tile; ++t) u0 += static_cast<int64_t>(tile_units(a.plan, rows, t)) * a.plan.head_blocks;
-      const int32_t tu = tile_units(a.plan, rows, tile);
-      u0 += static_cast<int64_t>(hk >> a.heads_log2) * tu;
-      ranges = Ranges::of(a.plan, units);
-      first = max(ranges.holder(u0), 0);
-      last = min(ranges.holder(u0 + tu - 1), ranges.blocks - 1);
-      work = first < last;
+  if (JW == 1) {
+    const int32_t c = blockIdx.y;
+    if (c + 1 >= ranges.blocks) return;
+    const int64_t u = ranges.start(c + 1) - 1;           // the last unit of the range
+    int32_t n = 0;
+    for (int32_t j = lane; j < v.batch; j += 32) n += a.prefix[j + 1] <= u ? 1 : 0;
+    int32_t b = __reduce_add_sync(0xffffffffu, n);
+    const Item it = find_item<false>(v, a.plan, a.prefix, u, 1, &b);
+    const int32_t tu = tile_units(a.plan, it.rows, it.tile);
+    u0 = u - it.unit;
+    first = ranges.holder(u0);
+    last = ranges.holder(u0 + tu - 1);
+    if (first != c || last == c) return;
+    const int32_t k = blockIdx.x * 8 + warp;             // row of the item: head of the block, row of the tile
+    hb = k / a.plan.rows;
+    r = k - hb * a.plan.rows;
+    const int64_t row = static_cast<int64_t>(it.tile) * a.plan.rows + r;
+    work = hb < (1 << a.heads_log2) && row < static_cast<int64_t>(it.rows.here) * a.plan.gq;
+    if (!work) return;
+    i = it.rows.first + static_cast<int32_t>(row / a.plan.gq);
+    h = ((it.block << a.heads_log2) + hb) * a.plan.gq + static_cast<int32_t>(row % a.plan.gq);
+  } else {
+    const int64_t job = blockIdx.x / (D / 32);
+    i = static_cast<int32_t>(job / a.q_heads);
+    h = static_cast<int32_t>(job % a.q_heads);
+    const int32_t b = kv_seq_of_row(v, i);
+    if (b < v.batch) {
+      const SeqRows rows = seq_rows(v, b);
+      const int32_t ti = i - rows.first;
+      if (ti >= 0 && ti < rows.here) {
+        const int hk = h / a.plan.gq;
+        const int64_t row = static_cast<int64_t>(ti) * a.plan.gq + h % a.plan.gq;
+        const int32_t tile = static_cast<int32_t>(row / a.plan.rows);
+        r = static_cast<int32_t>(row % a.plan.rows);
+        hb = hk & ((1 << a.heads_log2) - 1);
+        u0 = a.prefix[b];
+        for (int32_t t = 0; t < tile; ++t)
+          u0 += static_cast<int64_t>(tile_units(a.plan, rows, t)) * a.plan.head_blocks;
+        const int32_t tu = tile_units(a.plan, rows, tile);
+        u0 += static_cast<int64_t>(hk >> a.heads_log2) * tu;
+        first = ranges.holder(u0);
+        last = ranges.holder(u0 + tu - 1);
+        work = first < last;
+      }
     }
   }
-  if (JW == 1 && !work) return;                          // (JW > 1: the block meets below)
+  first = max(first, 0);
+  last = min(last, ranges.blocks - 1);
   float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
@@ -502,14 +466,12 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
         p = part_at(a, blk, ranges.start(blk) >= u0 ? 0 : 1, hb, r);
         x = a.part_ml[p];
       }
-      float top = x.x;
+      float top = x.y != 0.0f ? x.x : -INFINITY;         // a part without a key has no m (a row of NaN has l)
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
       const float m1 = fmaxf(m, top);
       const float keep = m == m1 ? 1.0f : exp2_fast(m - m1);
-      const float f = x.x == m1 ? 1.0f : exp2_fast(x.x - m1);
-      // a part without a key (m = -inf) counts nothing; l tells (a row of NaN has one)
-      const float mine = x.y == 0.0f ? 0.0f : f;
+      const float mine = x.y == 0.0f ? 0.0f : x.x == m1 ? 1.0f : exp2_fast(x.x - m1);
       float ls = x.y * mine;
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
@@ -559,7 +521,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
 }
 
 struct SplitSizes {
-  int nc, heads_log2, blocks, unit;
+  int nc, heads_log2, blocks, unit, rows;
+  bool prefill;                                // kv_prefill.cu
   bool whole;                                  // no item is cut: nothing to join
   int64_t prefix_bytes, ml_bytes, bytes;
 };
@@ -569,13 +532,29 @@ struct SplitSizes {
 // most kWholePieces pieces a warp.  Elsewhere eight heads a block: warps that read the same tokens' scales
 // share their sectors (one head a block: 64 us instead of 58 for one sequence of 131072 tokens, 64/8 heads).
 constexpr int kWholePieces = 8;
+// Rows of a sequence and key head (on average) up to which the codes go through registers; beyond, through
+// shared memory to tcgen05.
+constexpr int kFewRows = 16;
 
 SplitSizes split_sizes(const KvView& v, int32_t q_heads) {
   SplitSizes s{};
   const int gq = q_heads / v.heads;
   const int64_t rows = (static_cast<int64_t>(v.tokens) * gq + v.batch - 1) / v.batch;   // of a sequence, on average
+  s.prefill = rows > kFewRows && kv_prefill_takes(v);
   s.nc = rows > 8 && v.head_dim <= 128 ? 2 : 1;
-  s.blocks = sm_count() * (v.head_dim == 256 || s.nc == 2 ? 1 : 2);
+  s.rows = s.prefill ? kv_prefill_rows(v.head_dim) : 8 * s.nc;
+  s.blocks = sm_count() * (s.prefill || v.head_dim == 256 || s.nc == 2 ? 1 : 2);
+  s.prefix_bytes = (8 * (static_cast<int64_t>(v.batch) + 1) + 255) / 256 * 256;
+  auto parts = [&] {
+    const int64_t n = (2ll * s.blocks << s.heads_log2) * s.rows;
+    s.ml_bytes = n * 8;
+    s.bytes = s.prefix_bytes + s.ml_bytes + n * v.head_dim * 4;
+  };
+  if (s.prefill) {
+    s.unit = 128;
+    parts();
+    return s;
+  }
   int most = 0;
   while (most < 3 && v.heads % (2 << most) == 0) ++most;
   const int64_t tiles = std::max<int64_t>(v.batch, (static_cast<int64_t>(v.tokens) * gq + 8 * s.nc - 1) / (8 * s.nc));
@@ -587,12 +566,21 @@ SplitSizes split_sizes(const KvView& v, int32_t q_heads) {
     step = kStep * (kWarps >> most);
   }
   s.unit = s.whole ? kWholePieces * step : step;
-  if (s.whole) return s;
-  s.prefix_bytes = (8 * (static_cast<int64_t>(v.batch) + 1) + 255) / 256 * 256;
-  const int64_t parts = (2ll * s.blocks << s.heads_log2) * 8 * s.nc;
-  s.ml_bytes = parts * 8;
-  s.bytes = s.prefix_bytes + s.ml_bytes + parts * v.head_dim * 4;
+  if (!s.whole) parts();
   return s;
+}
+
+// The kernel that joins what the ranges cut.
+template <int D>
+cudaError_t run_join(const SplitArgs& a, bool prefill, cudaStream_t stream) {
+  // few rows with many parts: eight warps a row
+  const int64_t rows = static_cast<int64_t>(a.v.tokens) * a.q_heads;
+  const int64_t items = std::max<int64_t>(1, static_cast<int64_t>(a.v.batch) * a.plan.head_blocks);
+  if (!prefill && rows <= 8 * sm_count() && a.plan.blocks > 8 * items)
+    return launch_pdl(kv_join_kernel<D, 8>, dim3(static_cast<unsigned>(rows * (D / 32))), dim3(256), 0, stream, 1, a);
+  const int64_t most = std::min<int64_t>(a.plan.rows, static_cast<int64_t>(a.v.tokens) * a.plan.gq);
+  const unsigned blocks = static_cast<unsigned>(a.heads_log2 == 0 ? (most + 7) / 8 : (a.plan.rows << a.heads_log2) / 8);
+  return launch_pdl(kv_join_kernel<D, 1>, dim3(blocks, a.plan.blocks), dim3(256), 0, stream, 1, a);
 }
 
 template <int D, int NC>
@@ -602,14 +590,18 @@ cudaError_t run_split(const SplitArgs& a, cudaStream_t stream) {
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv_split_kernel<D, NC>, dim3(a.plan.blocks), dim3(kThreads), smem, stream, 1, a);
-  if (e != cudaSuccess || a.prefix == nullptr) return e;
-  // rows of few sequences have many parts, and there are few of them: eight warps a row; else one
-  const int64_t rows = static_cast<int64_t>(a.v.tokens) * a.q_heads;
-  const int64_t items = std::max<int64_t>(1, static_cast<int64_t>(a.v.batch) * a.plan.head_blocks);
-  return rows <= 8 * sm_count() && a.plan.blocks > 8 * items
-             ? launch_pdl(kv_join_kernel<D, 8>, dim3(static_cast<unsigned>(rows * (D / 32))), dim3(256), 0, stream, 1, a)
-             : launch_pdl(kv_join_kernel<D, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream,
-                          1, a);
+  return e != cudaSuccess || a.prefix == nullptr ? e : run_join<D>(a, false, stream);
+}
+
+template <int D>
+cudaError_t run_attention(const SplitArgs& a, const SplitSizes& s, cudaStream_t stream) {
+  if (s.prefill) {
+    const cudaError_t e = launch_kv_prefill(a, stream);
+    return e != cudaSuccess ? e : run_join<D>(a, true, stream);
+  }
+  if constexpr (D <= 128)
+    if (s.nc == 2) return run_split<D, 2>(a, stream);
+  return run_split<D, 1>(a, stream);
 }
 
 }  // namespace
@@ -621,7 +613,7 @@ qr_status launch_kv_attention(const KvView& v, const KvAttentionJob& j, cudaStre
   SplitArgs a{};
   a.v = v;
   a.plan.gq = j.q_heads / v.heads;
-  a.plan.rows = 8 * s.nc;
+  a.plan.rows = s.rows;
   a.plan.unit = s.unit;
   a.plan.head_blocks = v.heads >> s.heads_log2;
   a.plan.blocks = s.blocks;
@@ -639,10 +631,10 @@ qr_status launch_kv_attention(const KvView& v, const KvAttentionJob& j, cudaStre
   a.heads_log2 = s.heads_log2;
   cudaError_t e;
   switch (v.head_dim) {
-    case 32: e = s.nc == 2 ? run_split<32, 2>(a, stream) : run_split<32, 1>(a, stream); break;
-    case 64: e = s.nc == 2 ? run_split<64, 2>(a, stream) : run_split<64, 1>(a, stream); break;
-    case 128: e = s.nc == 2 ? run_split<128, 2>(a, stream) : run_split<128, 1>(a, stream); break;
-    default: e = run_split<256, 1>(a, stream); break;
+    case 32: e = run_attention<32>(a, s, stream); break;
+    case 64: e = run_attention<64>(a, s, stream); break;
+    case 128: e = run_attention<128>(a, s, stream); break;
+    default: e = run_attention<256>(a, s, stream); break;
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? QR_OK : QR_ERR_CUDA;

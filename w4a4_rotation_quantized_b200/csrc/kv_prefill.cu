@@ -1,0 +1,511 @@
+// kv_prefill.cu -- attention over the paged 4-bit KV cache for many query rows a key head
+// (prompts, chunks of prompts, drafts, cross attention): tensor-bound, 4 d operations a pair of
+// query row and key.
+//
+// A block takes one key head and two tiles of 128 query rows (token, head of the group; one tile where a head
+// is 256 wide) over a range of keys, 128 at a time:
+//   S = Q K^T     tcgen05, both operands in shared memory, 128 x 128 fp32 in tensor memory
+//   W = 2^(y - m) softmax warps, one row a thread, written back over S as fp16
+//   O += W V      tcgen05, W from tensor memory, V rows as they stand (MN-major), O in tensor memory
+// Codes become fp16 operands in shared memory as the whole numbers c - z, exact (kv_mma.cuh); the scales stay out
+// of them: with y_t = s_k (q . (c - z)) scale log2 e + log2 s_v the weight 2^(y - m) carries the value's scale, and
+// l = sum 2^(y - m) / s_v.  m follows the maximum of y with a lag of 8, so that weights stay below 2^8 in fp16 and
+// those that matter are not small ones, whatever the scales are; log2 s_v is held to [-40, 40], a value scale
+// below 2^-40 counts as 0.  Zeros beyond +-900 leave remainders, added to the scores and taken from the
+// outputs apart, in a second version of the softmax loops that such blocks of keys take.
+//
+// 17 warps: two softmax warpgroups (one a tile), eight warps that load and unpack the next keys, one that issues
+// the matrix instructions: while one tile is in its softmax the tensor cores have the other.  Two tiles share
+// an unpacked key tile; unpacking costs 11 instructions for 8 codes and thread, 0.35 of the tensor time of a tile
+// pair.  Work is shared out and joined as in kv_split.cuh.
+#include <algorithm>
+#include <cmath>
+
+#include "kv_mma.cuh"
+#include "kv_split_args.cuh"
+#include "qr_internal.h"
+
+namespace qr {
+
+namespace {
+
+constexpr int kKeys = 128;                     // keys of a block step
+constexpr int kSoftmaxThreads = 128;           // of a tile
+constexpr int kUnpackThreads = 256;
+constexpr int kThreadsP = 2 * kSoftmaxThreads + kUnpackThreads + 32;
+constexpr int kMaxBatch = 2048;
+
+template <int D>
+struct Shape {
+  static constexpr int kTiles = D == 256 ? 1 : 2;
+  static constexpr int kStages = D == 256 ? 1 : 2;
+  static constexpr int kSubs = D < 64 ? 1 : D / 64;           // 128-byte columns of a row
+  static constexpr int kTile = kSubs * 16384;                 // 128 rows
+  static constexpr int kQ = kTiles * kTile;
+  static constexpr int kStage = 2 * kTile;                    // keys, values
+  static constexpr int kCols = 5 * kKeys * 4 + 32;            // numbers of the keys of a stage
+  static constexpr int kBytes = kQ + kStages * kStage + kStages * kCols + 256;
+  static constexpr int kWords = D / 16;                       // code words of a thread (half a token's row)
+};
+
+// Column numbers of a stage.
+struct Cols {
+  float *sk, *lv, *rsv, *rk, *rv;
+  int32_t* rest;                               // [4]: any remainder among a warp's 32 keys
+  __device__ __forceinline__ explicit Cols(uint8_t* p) {
+    sk = reinterpret_cast<float*>(p);
+    lv = sk + kKeys;
+    rsv = lv + kKeys;
+    rk = rsv + kKeys;
+    rv = rk + kKeys;
+    rest = reinterpret_cast<int32_t*>(rv + kKeys);
+  }
+};
+
+enum Bar { kQFull = 0, kKFull = 1, kVFull = 3, kFree = 5, kSFull = 7, kPFull = 9, kODone = 11, kBars = 13 };
+
+// Byte of the 16-byte chunk `chunk` (of 8 elements) of row r in a swizzled tile of 128 rows.
+__device__ __forceinline__ int tile_at(int r, int chunk) {
+  return (chunk >> 3) * 16384 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArgs a, int32_t* status) {
+  using P = Shape<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+  uint8_t* q_tile = smem;
+  uint8_t* kv_tile = smem + P::kQ;
+  uint8_t* cols_at = kv_tile + P::kStages * P::kStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(cols_at + P::kStages * P::kCols);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
+  int64_t* prefix = reinterpret_cast<int64_t*>(cols_at + P::kStages * P::kCols + 256);
+  const KvView& v = a.v;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    mbar_init(&bars[kQFull], kUnpackThreads);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars[kKFull + i], kUnpackThreads);
+      mbar_init(&bars[kVFull + i], kUnpackThreads);
+      mbar_init(&bars[kFree + i], 1);
+      mbar_init(&bars[kSFull + i], 1);
+      mbar_init(&bars[kPFull + i], kSoftmaxThreads);
+      mbar_init(&bars[kODone + i], 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 16) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  grid_dep_wait();
+  grid_dep_launch();
+  split_prefix<kThreadsP>(v, a.plan, prefix);
+  const int64_t units = prefix[v.batch];
+  if (blockIdx.x == 0)
+    for (int32_t b = tid; b <= v.batch; b += kThreadsP) a.prefix[b] = prefix[b];
+  const Ranges ranges = Ranges::of(a.plan, units);
+  const int64_t start = ranges.start(blockIdx.x);
+  const int32_t count = ranges.count(blockIdx.x);
+
+  auto wait = [&](int bar, uint32_t n, int32_t code) -> bool {      // the n-th completion (from 0)
+    return mbar_wait_bounded(&bars[bar], n & 1, abort_flag, status, code);
+  };
+  auto wait_warp = [&](int bar, uint32_t n, int32_t code) -> bool {  // ... by a whole warp, with one answer
+    return __all_sync(0xffffffffu, wait(bar, n, code));
+  };
+
+  uint32_t steps = 0, segments = 0;              // key tiles and items so far
+  uint32_t tile_steps[2] = {0, 0};               // ... that tile 0 and 1 took part in
+  int32_t b = 0;
+  for (int32_t done = 0; done < count; ++segments) {
+    const Item it = find_item(v, a.plan, prefix, start + done, count - done, &b);
+    const SeqRows& rows = it.rows;
+    const int32_t row0 = it.tile * a.plan.rows, all_rows = rows.here * a.plan.gq;
+    const int tiles = P::kTiles == 2 && row0 + 128 < all_rows ? 2 : 1;
+    const int head = it.block;
+    const int32_t t_first = it.unit * kKeys;
+    bool ok = true;
+
+    if (warp < 8) {
+      // ------------------------------------------------------------- softmax
+      const int t = warp >> 2;
+      if (t < tiles) {
+        const int r = 128 * t + (warp & 3) * 32 + lane;
+        const int32_t rr = row0 + r;
+        const bool has = rr < all_rows;
+        const int32_t limit = has ? seen(rows, rr / a.plan.gq, a.plan.causal) : 0;
+        const int32_t all_limit = seen(rows, (row0 + 128 * t) / a.plan.gq, a.plan.causal);
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;        // 32 (warp & 3) in the lane field
+        const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + t * D;
+        const __half* q_row = has ? a.q + (rows.first + rr / a.plan.gq) * a.ldq +
+                                        static_cast<int64_t>(head * a.plan.gq + rr % a.plan.gq) * D : nullptr;
+        float m = 0.0f, l = 0.0f, zs = 0.0f, qsum = 0.0f;
+        bool started = false, summed = false;
+        for (int32_t j = 0; j < it.take && ok; ++j) {
+          const uint32_t n = steps + j, nt = tile_steps[t] + j;
+          const int st = n % P::kStages;
+          ok = wait_warp(kKFull + st, n / P::kStages, kDevTimeoutEpilogue) && wait_warp(kSFull + t, nt, kDevTimeoutEpilogue);
+          if (!ok) break;
+          tc_fence_after();
+          const Cols cols(cols_at + st * P::kCols);
+          const int32_t t0 = t_first + j * kKeys;
+          const int4 rest4 = *reinterpret_cast<const int4*>(cols.rest);
+          const bool rest = (rest4.x | rest4.y | rest4.z | rest4.w) != 0;
+          const bool plain = t0 + kKeys <= all_limit && !rest;
+          if (rest && !summed) {                         // sum of the row's queries, for remainders of key zeros
+            summed = true;
+            if (q_row != nullptr)
+              for (int e = 0; e < D; e += 8) {
+                const uint4 x = *reinterpret_cast<const uint4*>(q_row + e);
+                const __half2* h = reinterpret_cast<const __half2*>(&x);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 f = __half22float2(h[i]);
+                  qsum += f.x + f.y;
+                }
+              }
+          }
+          // y of four columns from their sums
+          auto four = [&](const uint32_t* s, int col, float (&y)[4]) {
+            const float4 sk = *reinterpret_cast<const float4*>(cols.sk + col);
+            const float4 lv = *reinterpret_cast<const float4*>(cols.lv + col);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), f2_pack(sk.x, sk.y),
+                             f2_pack(lv.x, lv.y)), y[0], y[1]);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), f2_pack(sk.z, sk.w),
+                             f2_pack(lv.z, lv.w)), y[2], y[3]);
+          };
+          auto four_slow = [&](const uint32_t* s, int col, float (&y)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x = fmaf(-cols.rk[col + i], qsum, __uint_as_float(s[i]));
+              y[i] = t0 + col + i < limit ? fmaf(x, cols.sk[col + i], cols.lv[col + i]) : -INFINITY;
+            }
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t s[32];
+            tmem_ld_32x32b_x32(s_at + 32 * ch, s);
+            tmem_ld_wait();
+            if (plain) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float y[4];
+                four(s + i, 32 * ch + i, y);
+                top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float y[4];
+                four_slow(s + i, 32 * ch + i, y);
+                top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
+              }
+            }
+          }
+          if (__any_sync(0xffffffffu, started ? top > m + 8.0f : top != -INFINITY)) {
+            const bool grows = started && top > m;
+            const float f = grows ? exp2_fast(m - top) : 1.0f;
+            if (grows || (!started && top != -INFINITY)) m = top;
+            started |= top != -INFINITY;
+            if (j > 0 && __any_sync(0xffffffffu, grows)) {
+              l *= f;
+              zs *= f;
+              ok = wait_warp(kODone + t, nt - 1, kDevTimeoutEpilogue);            // O is complete up to here
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int ch = 0; ch < D / 32; ++ch) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(o_at + 32 * ch, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st_32x32b_x32(o_at + 32 * ch, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          const uint64_t nm = f2_pack(-m, -m);
+          uint64_t l2 = 0;
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t s[32], w[16];
+            tmem_ld_32x32b_x32(s_at + 32 * ch, s);
+            tmem_ld_wait();
+            if (plain) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float y[4];
+                four(s + i, 32 * ch + i, y);
+                const float4 r = *reinterpret_cast<const float4*>(cols.rsv + 32 * ch + i);
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                  float y0, y1;
+                  f2_unpack(f2_add(f2_pack(y[k], y[k + 1]), nm), y0, y1);
+                  y0 = exp2_fast(y0);
+                  y1 = exp2_fast(y1);
+                  l2 = f2_fma(f2_pack(y0, y1), k == 0 ? f2_pack(r.x, r.y) : f2_pack(r.z, r.w), l2);
+                  const __half2 h = __floats2half2_rn(y0, y1);
+                  w[(i + k) / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float y[4];
+                four_slow(s + i, 32 * ch + i, y);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int col = 32 * ch + i + k;
+                  y[k] = exp2_fast(y[k] - m);
+                  l = fmaf(y[k], cols.rsv[col], l);
+                  const float rv = cols.rv[col];
+                  if (rv != 0.0f && y[k] != 0.0f) zs = fmaf(y[k], rv, zs);   // (NaN for a scale that is none)
+                }
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                  const __half2 h = __floats2half2_rn(y[k], y[k + 1]);
+                  w[(i + k) / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+              }
+            }
+            tmem_st_32x32b_x16(s_at + 16 * ch, w);         // over columns that have been read
+          }
+          float l0, l1;
+          f2_unpack(l2, l0, l1);
+          l += l0 + l1;
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&bars[kPFull + t]);
+        }
+        if (ok) ok = wait_warp(kODone + t, tile_steps[t] + it.take - 1, kDevTimeoutEpilogue);
+        if (ok) {
+          tc_fence_after();
+          const int64_t token = rows.first + rr / a.plan.gq;
+          const int h = head * a.plan.gq + rr % a.plan.gq;
+          const int64_t part = part_at(a, blockIdx.x, done == 0 ? 0 : 1, 0, r);
+          const float inv = it.whole ? inverse_or_zero(l) : 1.0f;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(o_at + 32 * ch, o);
+            tmem_ld_wait();
+            if (!has) continue;
+            // columns of a chunk of 8 hold elements 0 4 1 5 2 6 3 7
+            float y[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              y[i] = (__uint_as_float(o[(i & 24) + ((i & 3) << 1) + ((i >> 2) & 1)]) - zs) * inv;
+            if (it.whole) {
+              store_half<32>(a.out + token * a.ldo + h * D + 32 * ch, y);
+            } else {
+              float4* to = reinterpret_cast<float4*>(a.part_o + part * D + 32 * ch);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) to[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            }
+          }
+          if (has) {
+            if (!it.whole) a.part_ml[part] = make_float2(m, l);
+            else if (a.lse != nullptr) a.lse[token * a.q_heads + h] = row_lse(m, l);
+          }
+        }
+      }
+      tc_fence_before();
+    } else if (warp < 16) {
+      // ------------------------------------------------- queries, keys, values
+      const int u = tid - 2 * kSoftmaxThreads, tok = u & 127, half = u >> 7;
+      // queries: row tok of each tile, half of its chunks; elements of a chunk in the order 0 4 1 5 2 6 3 7
+      for (int t = 0; t < tiles; ++t) {
+        const int32_t rr = row0 + 128 * t + tok;
+        const __half* from = rr < all_rows ? a.q + (rows.first + rr / a.plan.gq) * a.ldq +
+                                                 static_cast<int64_t>(head * a.plan.gq + rr % a.plan.gq) * D : nullptr;
+#pragma unroll 4
+        for (int i = 0; i < D / 16; ++i) {
+          const int chunk = half * (D / 16) + i;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (from != nullptr) x = *reinterpret_cast<const uint4*>(from + chunk * 8);
+          *reinterpret_cast<uint4*>(q_tile + t * P::kTile + tile_at(tok, chunk)) =
+              make_uint4(byte_perm(x.x, x.z, 0x5410), byte_perm(x.x, x.z, 0x7632), byte_perm(x.y, x.w, 0x5410),
+                         byte_perm(x.y, x.w, 0x7632));
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[kQFull]);
+
+      const int64_t row_bytes = v.width >> 1;
+      const int at = head * (D / 2) + half * (D / 4);
+      const int group = head * D / v.group;
+      struct Keys {
+        uint32_t k[P::kWords], x[P::kWords];     // codes of half a token's key and value
+        float sk, sv;
+        int32_t zk, zv;
+        bool is;
+      };
+      auto slot_of = [&](int32_t j) -> int64_t {
+        const int32_t t = t_first + j * kKeys + tok;
+        return j < it.take && t < it.seen ? kv_slot(v, v.table, b, t) : -1;
+      };
+      auto load = [&](int64_t slot, Keys& x) {
+        x.is = slot >= 0;
+        const int64_t s = max(slot, static_cast<int64_t>(0));
+        const uint32_t* k = reinterpret_cast<const uint32_t*>(v.codes[0] + s * row_bytes + at);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v.codes[1] + s * row_bytes + at);
+        constexpr int W = P::kWords;
+        if constexpr (W >= 4) {
+#pragma unroll
+          for (int i = 0; i < W / 4; ++i) {
+            reinterpret_cast<uint4*>(x.k)[i] = reinterpret_cast<const uint4*>(k)[i];
+            reinterpret_cast<uint4*>(x.x)[i] = reinterpret_cast<const uint4*>(w)[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            x.k[i] = k[i];
+            x.x[i] = w[i];
+          }
+        }
+        const int64_t g = s * v.groups + group;
+        x.sk = v.scales[0][g];
+        x.zk = v.zeros[0][g];
+        x.sv = v.scales[1][g];
+        x.zv = v.zeros[1][g];
+      };
+      // (no page at all: nothing is held, and nothing may be read)
+      Keys next{};
+      int64_t slot = slot_of(0);
+      if (v.pages > 0) load(slot, next);
+      slot = slot_of(1);
+      for (int32_t j = 0; j < it.take && ok; ++j) {
+        const uint32_t n = steps + j;
+        const int st = n % P::kStages;
+        const Keys cur = next;
+        if (j + 1 < it.take && v.pages > 0) load(slot, next);
+        slot = slot_of(j + 2);
+        if (n >= P::kStages) ok = wait_warp(kFree + st, n / P::kStages - 1, kDevTimeoutProducer);
+        if (!ok) break;
+        uint8_t* kt = kv_tile + st * P::kStage;
+        uint8_t* vt = kt + P::kTile;
+        const int32_t zk = min(max(cur.zk, -900), 900), zv = min(max(cur.zv, -900), 900);
+        const bool none = !(cur.sv <= 0x1p40f), zero = cur.sv < 0x1p-40f;
+        if (half == 0) {
+          const Cols cols(cols_at + st * P::kCols);
+          const float lv = fminf(fmaxf(__log2f(cur.sv), -40.0f), 40.0f);
+          const float rv = none ? NAN : zero ? 0.0f : static_cast<float>(static_cast<int64_t>(cur.zv) - zv);
+          const float rk = static_cast<float>(static_cast<int64_t>(cur.zk) - zk);
+          cols.sk[tok] = cur.is ? cur.sk * a.scale_log2 : 0.0f;
+          cols.lv[tok] = cur.is ? lv : -INFINITY;
+          cols.rsv[tok] = cur.is ? exp2_fast(-lv) : 0.0f;
+          cols.rk[tok] = cur.is ? rk : 0.0f;
+          cols.rv[tok] = cur.is ? rv : 0.0f;
+          const bool any = __any_sync(0xffffffffu, cur.is && (rk != 0.0f || rv != 0.0f));
+          if (lane == 0) cols.rest[tok >> 5] = any;
+        }
+        auto unpack = [&](const uint32_t* w, int32_t z, bool blank, uint8_t* tile) {
+          const __half2 c1 = __half2half2(__int2half_rn(-1032 - z)), c0 = __half2half2(__int2half_rn(-72 - z));
+          const uint32_t z1024 = *reinterpret_cast<const uint32_t*>(&c1), z64 = *reinterpret_cast<const uint32_t*>(&c0);
+#pragma unroll
+          for (int i = 0; i < P::kWords; ++i) {
+            const uint32_t x = w[i], y = x >> 8;
+            uint4 e = make_uint4(add_half2(nib_1024(x), z1024), add_half2(nib_64(x), z64),
+                                 add_half2(nib_1024(y), z1024), add_half2(nib_64(y), z64));
+            if (blank) e = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(tile + tile_at(tok, half * P::kWords + i)) = e;
+          }
+        };
+        unpack(cur.k, zk, false, kt);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kKFull + st]);
+        unpack(cur.x, zv, zero || !cur.is, vt);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kVFull + st]);
+      }
+    } else if (lane == 0) {
+      // ------------------------------------------------------------ MMA issue
+      constexpr uint32_t kIdescS = idesc_f16(kKeys);
+      constexpr uint32_t kIdescO = idesc_f16(D) | (1u << 16);          // B with N contiguous
+      const uint32_t q0 = smem_u32(q_tile), kv0 = smem_u32(kv_tile);
+      auto scores = [&](int t, int st) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+          mma_f16(tmem + 128 * t, smem_desc_kmajor(q0 + t * P::kTile + off, 128),
+                  smem_desc_kmajor(kv0 + st * P::kStage + off, 128), kIdescS, k > 0);
+        }
+        mma_commit(&bars[kSFull + t]);
+      };
+      ok = wait(kQFull, segments, kDevTimeoutMma) &&
+           wait(kKFull + steps % P::kStages, steps / P::kStages, kDevTimeoutMma);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < tiles; ++t) scores(t, steps % P::kStages);
+      }
+      for (int32_t j = 0; j < it.take && ok; ++j) {
+        const uint32_t n = steps + j;
+        const int st = n % P::kStages;
+        ok = wait(kVFull + st, n / P::kStages, kDevTimeoutMma);
+        for (int t = 0; t < tiles && ok; ++t) {
+          if (!(ok = wait(kPFull + t, tile_steps[t] + j, kDevTimeoutMma))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < kKeys / 16; ++s)
+            mma_f16_ts(tmem + 256 + t * D, tmem + 128 * t + 8 * s,
+                       smem_desc_mn_sw128(kv0 + st * P::kStage + P::kTile + 2048 * s, 16384), kIdescO,
+                       j > 0 || s > 0);
+          mma_commit(&bars[kODone + t]);
+          if (t == tiles - 1) mma_commit(&bars[kFree + st]);
+          if (j + 1 < it.take) {
+            if (t == 0) {
+              if (!(ok = wait(kKFull + (n + 1) % P::kStages, (n + 1) / P::kStages, kDevTimeoutMma))) break;
+              tc_fence_after();
+            }
+            scores(t, (n + 1) % P::kStages);
+          }
+        }
+      }
+    }
+    steps += it.take;
+    tile_steps[0] += it.take;
+    if (tiles == 2) tile_steps[1] += it.take;
+    done += it.take;
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_flag) break;
+  }
+  __syncthreads();
+  if (warp == 16) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t run_prefill(const SplitArgs& a, cudaStream_t stream) {
+  const int smem = Shape<D>::kBytes + 1024 + (a.v.batch + 1) * static_cast<int>(sizeof(int64_t));
+  cudaError_t e = cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv_prefill_kernel<D>, dim3(a.plan.blocks), dim3(kThreadsP), smem, stream, 1, a,
+                    device_status_word());
+}
+
+}  // namespace
+
+bool kv_prefill_takes(const KvView& v) { return v.batch <= kMaxBatch; }
+int kv_prefill_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
+
+cudaError_t launch_kv_prefill(const SplitArgs& a, cudaStream_t stream) {
+  switch (a.v.head_dim) {
+    case 32: return run_prefill<32>(a, stream);
+    case 64: return run_prefill<64>(a, stream);
+    case 128: return run_prefill<128>(a, stream);
+    default: return run_prefill<256>(a, stream);
+  }
+}
+
+}  // namespace qr
