@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
 
   grid_dep_wait();
   grid_dep_launch();
-  split_prefix<kThreads>(v, a.plan, prefix);
+  split_prefix<kThreads, false>(v, a.plan, prefix);
   const int64_t units = prefix[v.batch];
   if (blockIdx.x == 0 && a.prefix != nullptr)
     for (int32_t b = threadIdx.x; b <= v.batch; b += kThreads) a.prefix[b] = prefix[b];
@@ -387,12 +387,68 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
 
 // Adds up the parts of items that were cut.  JW = 1: one warp a row, its lanes the elements of the head; a block
 // looks after the item that range blockIdx.y is the first to hold and not the last, if there is one, and
-// takes eight of its rows (token, query head).  JW = 8, for few rows with many parts: one block a row and 32
+// takes kJoinRows of its rows (token, query head).  JW = 8, for few rows with many parts: one block a row and 32
 // elements, its warps take every eighth part.
+constexpr int kJoinRows = 32;
+
+// The sum over the parts of ranges first, first + JW, .. last (from jw on) of a row: r of head hb of a block.
+template <int D, int JW, int E>
+__device__ __forceinline__ void join_parts(const SplitArgs& a, const Ranges& ranges, int64_t u0, int32_t first,
+                                           int32_t last, int jw, int hb, int r, int e0, float& m, float& l,
+                                           float (&o)[E]) {
+  constexpr int F = JW == 1 ? 8 : 16;                    // parts in flight
+  const int lane = threadIdx.x & 31;
+  m = -INFINITY;
+  l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  // 32 parts at a time: their m and l, one a lane, then their sums, several in flight
+  for (int32_t c0 = first; c0 <= last; c0 += 32 * JW) {
+    const int32_t blk = c0 + lane * JW + jw;
+    int64_t p = 0;
+    float2 x = make_float2(-INFINITY, 0.0f);
+    if (blk <= last) {
+      p = part_at(a, blk, ranges.start(blk) >= u0 ? 0 : 1, hb, r);
+      x = a.part_ml[p];
+    }
+    float top = x.y != 0.0f ? x.x : -INFINITY;           // a part without a key has no m (a row of NaN has l)
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float m1 = fmaxf(m, top);
+    const float keep = m == m1 ? 1.0f : exp2_fast(m - m1);
+    const float mine = x.y == 0.0f ? 0.0f : x.x == m1 ? 1.0f : exp2_fast(x.x - m1);
+    float ls = x.y * mine;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+    l = fmaf(l, keep, ls);
+    m = m1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= keep;
+    uint32_t left = __ballot_sync(0xffffffffu, x.y != 0.0f);
+    while (left != 0) {
+      float f8[F], y[F][E];
+#pragma unroll
+      for (int k = 0; k < F; ++k) {
+        const int from = left != 0 ? __ffs(left) - 1 : -1;
+        left &= left - 1;
+        const int64_t pk = __shfl_sync(0xffffffffu, p, max(from, 0));
+        f8[k] = __shfl_sync(0xffffffffu, mine, max(from, 0));
+        const float* src = a.part_o + pk * D;
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[k][e] = from >= 0 ? src[e0 + 32 * e] : 0.0f;
+        if (from < 0) f8[k] = 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < F; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(y[k][e], f8[k], o[e]);
+    }
+  }
+}
+
 template <int D, int JW>
 __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
   constexpr int E = JW == 1 ? D / 32 : 1;
-  constexpr int F = JW == 1 ? 8 : 16;                    // parts in flight
   __shared__ float acc[JW][32];
   __shared__ float2 ml[JW];
   const KvView& v = a.v;
@@ -402,9 +458,13 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
   grid_dep_launch();
   const int64_t units = a.prefix[v.batch];
   const Ranges ranges = Ranges::of(a.plan, units);
-  bool work = false;
-  int32_t i = 0, h = 0, first = 0, last = 0, r = 0, hb = 0;   // row, query head, ranges that hold the item, place
-  int64_t u0 = 0;
+  auto finish = [&](int32_t i, int32_t h, float m, float l, const float (&o)[E]) {
+    const float inv = inverse_or_zero(l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) a.out[i * a.ldo + h * D + e0 + 32 * e] = __float2half_rn(o[e] * inv);
+    if (a.lse != nullptr && e0 == 0) a.lse[static_cast<int64_t>(i) * a.q_heads + h] = row_lse(m, l);
+  };
+  float m, l, o[E];
   if (JW == 1) {
     const int32_t c = blockIdx.y;
     if (c + 1 >= ranges.blocks) return;
@@ -414,110 +474,49 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
     int32_t b = __reduce_add_sync(0xffffffffu, n);
     const Item it = find_item<false>(v, a.plan, a.prefix, u, 1, &b);
     const int32_t tu = tile_units(a.plan, it.rows, it.tile);
-    u0 = u - it.unit;
-    first = ranges.holder(u0);
-    last = ranges.holder(u0 + tu - 1);
+    const int64_t u0 = u - it.unit;
+    const int32_t first = ranges.holder(u0), last = min(ranges.holder(u0 + tu - 1), ranges.blocks - 1);
     if (first != c || last == c) return;
-    const int32_t k = blockIdx.x * 8 + warp;             // row of the item: head of the block, row of the tile
-    hb = k / a.plan.rows;
-    r = k - hb * a.plan.rows;
-    const int64_t row = static_cast<int64_t>(it.tile) * a.plan.rows + r;
-    work = hb < (1 << a.heads_log2) && row < static_cast<int64_t>(it.rows.here) * a.plan.gq;
-    if (!work) return;
-    i = it.rows.first + static_cast<int32_t>(row / a.plan.gq);
-    h = ((it.block << a.heads_log2) + hb) * a.plan.gq + static_cast<int32_t>(row % a.plan.gq);
-  } else {
-    const int64_t job = blockIdx.x / (D / 32);
-    i = static_cast<int32_t>(job / a.q_heads);
-    h = static_cast<int32_t>(job % a.q_heads);
-    const int32_t b = kv_seq_of_row(v, i);
-    if (b < v.batch) {
-      const SeqRows rows = seq_rows(v, b);
-      const int32_t ti = i - rows.first;
-      if (ti >= 0 && ti < rows.here) {
-        const int hk = h / a.plan.gq;
-        const int64_t row = static_cast<int64_t>(ti) * a.plan.gq + h % a.plan.gq;
-        const int32_t tile = static_cast<int32_t>(row / a.plan.rows);
-        r = static_cast<int32_t>(row % a.plan.rows);
-        hb = hk & ((1 << a.heads_log2) - 1);
-        u0 = a.prefix[b];
-        for (int32_t t = 0; t < tile; ++t)
-          u0 += static_cast<int64_t>(tile_units(a.plan, rows, t)) * a.plan.head_blocks;
-        const int32_t tu = tile_units(a.plan, rows, tile);
-        u0 += static_cast<int64_t>(hk >> a.heads_log2) * tu;
-        first = ranges.holder(u0);
-        last = ranges.holder(u0 + tu - 1);
-        work = first < last;
-      }
+    const int32_t all_rows = it.rows.here * a.plan.gq;
+#pragma unroll 1
+    for (int s = 0; s < kJoinRows / 8; ++s) {
+      const int32_t k = blockIdx.x * kJoinRows + s * 8 + warp;     // row of the item: head of the block, row of the tile
+      const int32_t hb = k / a.plan.rows, r = k - hb * a.plan.rows, row = it.tile * a.plan.rows + r;
+      if (hb >= (1 << a.heads_log2) || row >= all_rows) continue;
+      join_parts<D, 1, E>(a, ranges, u0, first, last, 0, hb, r, e0, m, l, o);
+      finish(it.rows.first + row / a.plan.gq, ((it.block << a.heads_log2) + hb) * a.plan.gq + row % a.plan.gq, m, l, o);
     }
+    return;
   }
-  first = max(first, 0);
-  last = min(last, ranges.blocks - 1);
-  float m = -INFINITY, l = 0.0f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  if (work) {
-    // 32 parts at a time: their m and l, one a lane, then their sums, several in flight
-    for (int32_t c0 = first; c0 <= last; c0 += 32 * JW) {
-      const int32_t blk = c0 + lane * JW + jw;
-      int64_t p = 0;
-      float2 x = make_float2(-INFINITY, 0.0f);
-      if (blk <= last) {
-        p = part_at(a, blk, ranges.start(blk) >= u0 ? 0 : 1, hb, r);
-        x = a.part_ml[p];
-      }
-      float top = x.y != 0.0f ? x.x : -INFINITY;         // a part without a key has no m (a row of NaN has l)
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-      const float m1 = fmaxf(m, top);
-      const float keep = m == m1 ? 1.0f : exp2_fast(m - m1);
-      const float mine = x.y == 0.0f ? 0.0f : x.x == m1 ? 1.0f : exp2_fast(x.x - m1);
-      float ls = x.y * mine;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
-      l = fmaf(l, keep, ls);
-      m = m1;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= keep;
-      uint32_t left = __ballot_sync(0xffffffffu, x.y != 0.0f);
-      while (left != 0) {
-        float f8[F], y[F][E];
-#pragma unroll
-        for (int k = 0; k < F; ++k) {
-          const int from = left != 0 ? __ffs(left) - 1 : -1;
-          left &= left - 1;
-          const int64_t pk = __shfl_sync(0xffffffffu, p, max(from, 0));
-          f8[k] = __shfl_sync(0xffffffffu, mine, max(from, 0));
-          const float* src = a.part_o + pk * D;
-#pragma unroll
-          for (int e = 0; e < E; ++e) y[k][e] = from >= 0 ? src[e0 + 32 * e] : 0.0f;
-          if (from < 0) f8[k] = 0.0f;
-        }
-#pragma unroll
-        for (int k = 0; k < F; ++k)
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = fmaf(y[k][e], f8[k], o[e]);
-      }
-    }
+  const int64_t job = blockIdx.x / (D / 32);
+  const int32_t i = static_cast<int32_t>(job / a.q_heads), h = static_cast<int32_t>(job % a.q_heads);
+  const int32_t b = kv_seq_of_row(v, i);
+  if (b >= v.batch) return;                              // (the whole block)
+  const SeqRows rows = seq_rows(v, b);
+  const int32_t ti = i - rows.first;
+  if (ti < 0 || ti >= rows.here) return;
+  const int hk = h / a.plan.gq;
+  const int32_t row = ti * a.plan.gq + h % a.plan.gq, tile = row / a.plan.rows;
+  int64_t u0 = a.prefix[b];
+  for (int32_t t = 0; t < tile; ++t) u0 += static_cast<int64_t>(tile_units(a.plan, rows, t)) * a.plan.head_blocks;
+  const int32_t tu = tile_units(a.plan, rows, tile);
+  u0 += static_cast<int64_t>(hk >> a.heads_log2) * tu;
+  const int32_t first = ranges.holder(u0), last = min(ranges.holder(u0 + tu - 1), ranges.blocks - 1);
+  if (first >= last) return;
+  join_parts<D, JW, E>(a, ranges, u0, first, last, jw, hk & ((1 << a.heads_log2) - 1), row % a.plan.rows, e0, m, l, o);
+  acc[jw][lane] = o[0];
+  if (lane == 0) ml[jw] = make_float2(m, l);
+  __syncthreads();
+  if (jw != 0) return;
+  for (int w = 0; w < JW; ++w) m = fmaxf(m, ml[w].x);
+  l = o[0] = 0.0f;
+  for (int w = 0; w < JW; ++w) {
+    const float2 x = ml[w];
+    const float f = x.y == 0.0f ? 0.0f : x.x == m ? 1.0f : exp2_fast(x.x - m);
+    l = fmaf(x.y, f, l);
+    o[0] = fmaf(acc[w][lane], f, o[0]);
   }
-  if (JW > 1) {
-    acc[jw][lane] = o[0];
-    if (lane == 0) ml[jw] = make_float2(m, l);
-    __syncthreads();
-    if (!work || jw != 0) return;
-    for (int w = 0; w < JW; ++w) m = fmaxf(m, ml[w].x);
-    l = o[0] = 0.0f;
-    for (int w = 0; w < JW; ++w) {
-      const float2 x = ml[w];
-      const float f = x.y == 0.0f ? 0.0f : x.x == m ? 1.0f : exp2_fast(x.x - m);
-      l = fmaf(x.y, f, l);
-      o[0] = fmaf(acc[w][lane], f, o[0]);
-    }
-  }
-  const float inv = inverse_or_zero(l);
-#pragma unroll
-  for (int e = 0; e < E; ++e) a.out[i * a.ldo + h * D + e0 + 32 * e] = __float2half_rn(o[e] * inv);
-  if (a.lse != nullptr && e0 == 0) a.lse[static_cast<int64_t>(i) * a.q_heads + h] = row_lse(m, l);
+  finish(i, h, m, l, o);
 }
 
 struct SplitSizes {
@@ -579,7 +578,8 @@ cudaError_t run_join(const SplitArgs& a, bool prefill, cudaStream_t stream) {
   if (!prefill && rows <= 8 * sm_count() && a.plan.blocks > 8 * items)
     return launch_pdl(kv_join_kernel<D, 8>, dim3(static_cast<unsigned>(rows * (D / 32))), dim3(256), 0, stream, 1, a);
   const int64_t most = std::min<int64_t>(a.plan.rows, static_cast<int64_t>(a.v.tokens) * a.plan.gq);
-  const unsigned blocks = static_cast<unsigned>(a.heads_log2 == 0 ? (most + 7) / 8 : (a.plan.rows << a.heads_log2) / 8);
+  const int64_t all = a.heads_log2 == 0 ? most : static_cast<int64_t>(a.plan.rows) << a.heads_log2;
+  const unsigned blocks = static_cast<unsigned>((all + kJoinRows - 1) / kJoinRows);
   return launch_pdl(kv_join_kernel<D, 1>, dim3(blocks, a.plan.blocks), dim3(256), 0, stream, 1, a);
 }
 

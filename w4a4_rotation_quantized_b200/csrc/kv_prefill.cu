@@ -9,17 +9,20 @@
 //   O += W V      tcgen05, W from tensor memory, V rows as they stand (MN-major), O in tensor memory
 // Codes become fp16 operands in shared memory as the whole numbers c - z, exact (kv_mma.cuh); the scales stay out
 // of them: with y_t = s_k (q . (c - z)) scale log2 e + log2 s_v the weight 2^(y - m) carries the value's scale, and
-// l = sum 2^(y - m) / s_v.  m follows the maximum of y with a lag of 8, so that weights stay below 2^8 in fp16 and
-// those that matter are not small ones, whatever the scales are; log2 s_v is held to [-40, 40], a value scale
+// l = sum 2^(y - m) / s_v.  m follows the maximum of y with a lag of up to 15, so that weights stay below 2^15 in fp16
+// and those that matter are not small ones, whatever the scales are; log2 s_v is held to [-40, 40], a value scale
 // below 2^-40 counts as 0.  Zeros beyond +-900 leave remainders, added to the scores and taken from the
 // outputs apart, in a second version of the softmax loops that such blocks of keys take.
 //
-// 17 warps: two softmax warpgroups (one a tile), eight warps that load and unpack the next keys, one that issues
-// the matrix instructions: while one tile is in its softmax the tensor cores have the other.  Two tiles share
-// an unpacked key tile; unpacking costs 11 instructions for 8 codes and thread, 0.35 of the tensor time of a tile
-// pair.  Work is shared out and joined as in kv_split.cuh.
+// 13 warps (so that a thread may have 128 registers): two softmax warpgroups (one a tile), four warps that load and
+// unpack the next keys, one token a thread, one that issues the matrix instructions: while one tile is in its
+// softmax the tensor cores have the other.  Two tiles share an unpacked key tile.  The softmax goes over the
+// scores once, with the maximum of the keys before: only when a weight would pass 2^15 it goes back, finds the
+// new maximum, rescales and starts over (the weights wait in registers until then, the scores in tensor
+// memory).  Work is shared out and joined as in kv_split.cuh.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv_mma.cuh"
 #include "kv_split_args.cuh"
@@ -31,7 +34,7 @@ namespace {
 
 constexpr int kKeys = 128;                     // keys of a block step
 constexpr int kSoftmaxThreads = 128;           // of a tile
-constexpr int kUnpackThreads = 256;
+constexpr int kUnpackThreads = 128;
 constexpr int kThreadsP = 2 * kSoftmaxThreads + kUnpackThreads + 32;
 constexpr int kMaxBatch = 2048;
 
@@ -45,7 +48,7 @@ struct Shape {
   static constexpr int kStage = 2 * kTile;                    // keys, values
   static constexpr int kCols = 5 * kKeys * 4 + 32;            // numbers of the keys of a stage
   static constexpr int kBytes = kQ + kStages * kStage + kStages * kCols + 256;
-  static constexpr int kWords = D / 16;                       // code words of a thread (half a token's row)
+  static constexpr int kWords = D / 8;                        // code words of a token's key, or its value
 };
 
 // Column numbers of a stage.
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 16) {
+  if (warp == 12) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -108,7 +111,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
 
   grid_dep_wait();
   grid_dep_launch();
-  split_prefix<kThreadsP>(v, a.plan, prefix);
+  split_prefix<kThreadsP, true>(v, a.plan, prefix);
   const int64_t units = prefix[v.batch];
   if (blockIdx.x == 0)
     for (int32_t b = tid; b <= v.batch; b += kThreadsP) a.prefix[b] = prefix[b];
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
         const __half* q_row = has ? a.q + (rows.first + rr / a.plan.gq) * a.ldq +
                                         static_cast<int64_t>(head * a.plan.gq + rr % a.plan.gq) * D : nullptr;
         float m = 0.0f, l = 0.0f, zs = 0.0f, qsum = 0.0f;
-        bool started = false, summed = false;
+        bool started = !has, summed = false;               // (rows of nobody hold nothing up)
         for (int32_t j = 0; j < it.take && ok; ++j) {
           const uint32_t n = steps + j, nt = tile_steps[t] + j;
           const int st = n % P::kStages;
@@ -174,116 +177,124 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
                 }
               }
           }
-          // y of four columns from their sums
-          auto four = [&](const uint32_t* s, int col, float (&y)[4]) {
+          const int32_t lim = limit - t0;
+          // y of four columns from their sums.  MODE 0: every row sees every key; 1: not so; 2: and zeros leave remainders
+          auto four = [&](auto mode, const uint32_t* s, int col, float (&y)[4]) {
+            constexpr int MODE = decltype(mode)::value;
             const float4 sk = *reinterpret_cast<const float4*>(cols.sk + col);
             const float4 lv = *reinterpret_cast<const float4*>(cols.lv + col);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), f2_pack(sk.x, sk.y),
-                             f2_pack(lv.x, lv.y)), y[0], y[1]);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), f2_pack(sk.z, sk.w),
-                             f2_pack(lv.z, lv.w)), y[2], y[3]);
-          };
-          auto four_slow = [&](const uint32_t* s, int col, float (&y)[4]) {
+            uint64_t x0 = f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1]));
+            uint64_t x1 = f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3]));
+            if constexpr (MODE == 2) {
+              const float4 rk = *reinterpret_cast<const float4*>(cols.rk + col);
+              x0 = f2_fma(f2_pack(-rk.x, -rk.y), f2_pack(qsum, qsum), x0);
+              x1 = f2_fma(f2_pack(-rk.z, -rk.w), f2_pack(qsum, qsum), x1);
+            }
+            f2_unpack(f2_fma(x0, f2_pack(sk.x, sk.y), f2_pack(lv.x, lv.y)), y[0], y[1]);
+            f2_unpack(f2_fma(x1, f2_pack(sk.z, sk.w), f2_pack(lv.z, lv.w)), y[2], y[3]);
+            if constexpr (MODE > 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float x = fmaf(-cols.rk[col + i], qsum, __uint_as_float(s[i]));
-              y[i] = t0 + col + i < limit ? fmaf(x, cols.sk[col + i], cols.lv[col + i]) : -INFINITY;
+              for (int i = 0; i < 4; ++i)
+                if (col + i >= lim) y[i] = -INFINITY;
             }
           };
-          float top = -INFINITY;
+          auto maximum = [&](auto mode) {
+            float top = -INFINITY;
 #pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t s[32];
-            tmem_ld_32x32b_x32(s_at + 32 * ch, s);
-            tmem_ld_wait();
-            if (plain) {
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t s[32];
+              tmem_ld_32x32b_x32(s_at + 32 * ch, s);
+              tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 float y[4];
-                four(s + i, 32 * ch + i, y);
-                top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float y[4];
-                four_slow(s + i, 32 * ch + i, y);
+                four(mode, s + i, 32 * ch + i, y);
                 top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
               }
             }
-          }
-          if (__any_sync(0xffffffffu, started ? top > m + 8.0f : top != -INFINITY)) {
-            const bool grows = started && top > m;
-            const float f = grows ? exp2_fast(m - top) : 1.0f;
-            if (grows || (!started && top != -INFINITY)) m = top;
-            started |= top != -INFINITY;
-            if (j > 0 && __any_sync(0xffffffffu, grows)) {
-              l *= f;
-              zs *= f;
-              ok = wait_warp(kODone + t, nt - 1, kDevTimeoutEpilogue);            // O is complete up to here
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int ch = 0; ch < D / 32; ++ch) {
-                uint32_t o[32];
-                tmem_ld_32x32b_x32(o_at + 32 * ch, o);
-                tmem_ld_wait();
+            return has ? top : -INFINITY;
+          };
+          uint32_t w[64];
+          float dl, dz;                                    // what this step adds to l and zs
+          auto weights = [&](auto mode) {                  // returns the maximum
+            constexpr int MODE = decltype(mode)::value;
+            const uint64_t nm = f2_pack(-m, -m);
+            uint64_t l2 = 0, l3 = 0;
+            float top = -INFINITY;
+            dz = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st_32x32b_x32(o_at + 32 * ch, o);
-              }
-              tmem_st_wait();
-            }
-          }
-          const uint64_t nm = f2_pack(-m, -m);
-          uint64_t l2 = 0;
-#pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t s[32], w[16];
-            tmem_ld_32x32b_x32(s_at + 32 * ch, s);
-            tmem_ld_wait();
-            if (plain) {
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t s[32];
+              tmem_ld_32x32b_x32(s_at + 32 * ch, s);
+              tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 float y[4];
-                four(s + i, 32 * ch + i, y);
-                const float4 r = *reinterpret_cast<const float4*>(cols.rsv + 32 * ch + i);
+                const int col = 32 * ch + i;
+                four(mode, s + i, col, y);
+                top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
+                const float4 r = *reinterpret_cast<const float4*>(cols.rsv + col);
+                f2_unpack(f2_add(f2_pack(y[0], y[1]), nm), y[0], y[1]);
+                f2_unpack(f2_add(f2_pack(y[2], y[3]), nm), y[2], y[3]);
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                  float y0, y1;
-                  f2_unpack(f2_add(f2_pack(y[k], y[k + 1]), nm), y0, y1);
-                  y0 = exp2_fast(y0);
-                  y1 = exp2_fast(y1);
-                  l2 = f2_fma(f2_pack(y0, y1), k == 0 ? f2_pack(r.x, r.y) : f2_pack(r.z, r.w), l2);
-                  const __half2 h = __floats2half2_rn(y0, y1);
-                  w[(i + k) / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                for (int k = 0; k < 4; ++k) y[k] = exp2_fast(y[k]);
+                l2 = f2_fma(f2_pack(y[0], y[1]), f2_pack(r.x, r.y), l2);
+                l3 = f2_fma(f2_pack(y[2], y[3]), f2_pack(r.z, r.w), l3);
+                if constexpr (MODE == 2) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const float rv = cols.rv[col + k];
+                    if (rv != 0.0f && y[k] != 0.0f) dz = fmaf(y[k], rv, dz);   // (NaN for a scale that is none)
+                  }
                 }
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float y[4];
-                four_slow(s + i, 32 * ch + i, y);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int col = 32 * ch + i + k;
-                  y[k] = exp2_fast(y[k] - m);
-                  l = fmaf(y[k], cols.rsv[col], l);
-                  const float rv = cols.rv[col];
-                  if (rv != 0.0f && y[k] != 0.0f) zs = fmaf(y[k], rv, zs);   // (NaN for a scale that is none)
-                }
-#pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                  const __half2 h = __floats2half2_rn(y[k], y[k + 1]);
-                  w[(i + k) / 2] = *reinterpret_cast<const uint32_t*>(&h);
-                }
+                const __half2 h0 = __floats2half2_rn(y[0], y[1]), h1 = __floats2half2_rn(y[2], y[3]);
+                w[col / 2] = *reinterpret_cast<const uint32_t*>(&h0);
+                w[col / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
               }
             }
-            tmem_st_32x32b_x16(s_at + 16 * ch, w);         // over columns that have been read
-          }
-          float l0, l1;
-          f2_unpack(l2, l0, l1);
-          l += l0 + l1;
+            float l0, l1;
+            f2_unpack(f2_add(l2, l3), l0, l1);
+            dl = l0 + l1;
+            return has ? top : -INFINITY;
+          };
+          auto step = [&](auto mode) -> bool {
+            for (bool exact = __any_sync(0xffffffffu, !started);; exact = true) {
+              if (exact) {
+                const float top = maximum(mode);
+                const bool grows = started && top > m;
+                const float f = grows ? exp2_fast(m - top) : 1.0f;
+                if (grows || (!started && top != -INFINITY)) m = top;
+                started |= top != -INFINITY;
+                if (__any_sync(0xffffffffu, grows)) {      // (never at the item's first keys)
+                  l *= f;
+                  zs *= f;
+                  if (!wait_warp(kODone + t, nt - 1, kDevTimeoutEpilogue)) return false;   // O is complete up to here
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int ch = 0; ch < D / 32; ++ch) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(o_at + 32 * ch, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st_32x32b_x32(o_at + 32 * ch, o);
+                  }
+                  tmem_st_wait();
+                }
+              }
+              const float top = weights(mode);
+              if (exact || !__any_sync(0xffffffffu, top > m + 15.0f)) break;
+            }
+            return true;
+          };
+          ok = plain ? step(std::integral_constant<int, 0>{})
+                     : rest ? step(std::integral_constant<int, 2>{}) : step(std::integral_constant<int, 1>{});
+          if (!ok) break;
+          l += dl;
+          zs += dz;
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch)                   // over columns that have been read
+            tmem_st_32x32b_x32(s_at + 32 * ch, *reinterpret_cast<const uint32_t(*)[32]>(w + 32 * ch));
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&bars[kPFull + t]);
@@ -321,17 +332,16 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
         }
       }
       tc_fence_before();
-    } else if (warp < 16) {
+    } else if (warp < 12) {
       // ------------------------------------------------- queries, keys, values
-      const int u = tid - 2 * kSoftmaxThreads, tok = u & 127, half = u >> 7;
-      // queries: row tok of each tile, half of its chunks; elements of a chunk in the order 0 4 1 5 2 6 3 7
+      const int tok = tid - 2 * kSoftmaxThreads;
+      // queries: row tok of each tile; elements of a chunk in the order 0 4 1 5 2 6 3 7
       for (int t = 0; t < tiles; ++t) {
         const int32_t rr = row0 + 128 * t + tok;
         const __half* from = rr < all_rows ? a.q + (rows.first + rr / a.plan.gq) * a.ldq +
                                                  static_cast<int64_t>(head * a.plan.gq + rr % a.plan.gq) * D : nullptr;
-#pragma unroll 4
-        for (int i = 0; i < D / 16; ++i) {
-          const int chunk = half * (D / 16) + i;
+#pragma unroll 8
+        for (int chunk = 0; chunk < D / 8; ++chunk) {
           uint4 x = make_uint4(0, 0, 0, 0);
           if (from != nullptr) x = *reinterpret_cast<const uint4*>(from + chunk * 8);
           *reinterpret_cast<uint4*>(q_tile + t * P::kTile + tile_at(tok, chunk)) =
@@ -342,92 +352,96 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
       fence_proxy_async_smem();
       mbar_arrive(&bars[kQFull]);
 
+      // one token a thread: its key's codes are loaded a step ahead, its value's while the key is unpacked
+      constexpr int W = P::kWords;
       const int64_t row_bytes = v.width >> 1;
-      const int at = head * (D / 2) + half * (D / 4);
-      const int group = head * D / v.group;
-      struct Keys {
-        uint32_t k[P::kWords], x[P::kWords];     // codes of half a token's key and value
-        float sk, sv;
-        int32_t zk, zv;
-        bool is;
-      };
+      const int at = head * (D / 2);
+      const uint32_t group = head * D / v.group;
       auto slot_of = [&](int32_t j) -> int64_t {
         const int32_t t = t_first + j * kKeys + tok;
         return j < it.take && t < it.seen ? kv_slot(v, v.table, b, t) : -1;
       };
-      auto load = [&](int64_t slot, Keys& x) {
-        x.is = slot >= 0;
-        const int64_t s = max(slot, static_cast<int64_t>(0));
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(v.codes[0] + s * row_bytes + at);
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(v.codes[1] + s * row_bytes + at);
-        constexpr int W = P::kWords;
-        if constexpr (W >= 4) {
+      auto load = [&](int side, int64_t slot, uint32_t (&x)[W]) {
+        if (v.pages == 0) return;                          // nothing is held, and nothing may be read
+        const uint4* from = reinterpret_cast<const uint4*>((side ? v.codes[1] : v.codes[0]) +
+                                                           max(slot, static_cast<int64_t>(0)) * row_bytes + at);
 #pragma unroll
-          for (int i = 0; i < W / 4; ++i) {
-            reinterpret_cast<uint4*>(x.k)[i] = reinterpret_cast<const uint4*>(k)[i];
-            reinterpret_cast<uint4*>(x.x)[i] = reinterpret_cast<const uint4*>(w)[i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            x.k[i] = k[i];
-            x.x[i] = w[i];
-          }
+        for (int i = 0; i < W / 4; ++i) {
+          const uint4 y = from[i];
+          x[4 * i] = y.x;
+          x[4 * i + 1] = y.y;
+          x[4 * i + 2] = y.z;
+          x[4 * i + 3] = y.w;
         }
-        const int64_t g = s * v.groups + group;
-        x.sk = v.scales[0][g];
-        x.zk = v.zeros[0][g];
-        x.sv = v.scales[1][g];
-        x.zv = v.zeros[1][g];
       };
-      // (no page at all: nothing is held, and nothing may be read)
-      Keys next{};
-      int64_t slot = slot_of(0);
-      if (v.pages > 0) load(slot, next);
-      slot = slot_of(1);
+      struct Numbers {
+        float sk, sv;
+        int32_t zk, zv;
+      };
+      auto numbers = [&](int64_t slot) {
+        Numbers x{};
+        if (v.pages > 0) {
+          const uint32_t g = static_cast<uint32_t>(max(slot, static_cast<int64_t>(0))) * v.groups + group;
+          x.sk = v.scales[0][g];
+          x.zk = v.zeros[0][g];
+          x.sv = v.scales[1][g];
+          x.zv = v.zeros[1][g];
+        }
+        return x;
+      };
+      auto unpack = [&](const uint32_t (&w)[W], int32_t z, bool blank, uint8_t* tile) {
+        const __half2 c1 = __half2half2(__int2half_rn(-1032 - z)), c0 = __half2half2(__int2half_rn(-72 - z));
+        const uint32_t z1024 = *reinterpret_cast<const uint32_t*>(&c1), z64 = *reinterpret_cast<const uint32_t*>(&c0);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const uint32_t x = w[i], y = x >> 8;
+          uint4 e = make_uint4(add_half2(nib_1024(x), z1024), add_half2(nib_64(x), z64),
+                               add_half2(nib_1024(y), z1024), add_half2(nib_64(y), z64));
+          if (blank) e = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(tile + tile_at(tok, i)) = e;
+        }
+      };
+      uint32_t kw[W] = {}, vw[W] = {};
+      int64_t slot = slot_of(0), next = slot_of(1);
+      load(0, slot, kw);
+      Numbers num = numbers(slot);
       for (int32_t j = 0; j < it.take && ok; ++j) {
         const uint32_t n = steps + j;
         const int st = n % P::kStages;
-        const Keys cur = next;
-        if (j + 1 < it.take && v.pages > 0) load(slot, next);
-        slot = slot_of(j + 2);
+        load(1, slot, vw);
+        const int64_t after = slot_of(j + 2);
         if (n >= P::kStages) ok = wait_warp(kFree + st, n / P::kStages - 1, kDevTimeoutProducer);
         if (!ok) break;
         uint8_t* kt = kv_tile + st * P::kStage;
         uint8_t* vt = kt + P::kTile;
-        const int32_t zk = min(max(cur.zk, -900), 900), zv = min(max(cur.zv, -900), 900);
-        const bool none = !(cur.sv <= 0x1p40f), zero = cur.sv < 0x1p-40f;
-        if (half == 0) {
+        const bool is = slot >= 0;
+        const int32_t zk = min(max(num.zk, -900), 900), zv = min(max(num.zv, -900), 900);
+        const bool none = !(num.sv <= 0x1p40f), zero = num.sv < 0x1p-40f;
+        {
           const Cols cols(cols_at + st * P::kCols);
-          const float lv = fminf(fmaxf(__log2f(cur.sv), -40.0f), 40.0f);
-          const float rv = none ? NAN : zero ? 0.0f : static_cast<float>(static_cast<int64_t>(cur.zv) - zv);
-          const float rk = static_cast<float>(static_cast<int64_t>(cur.zk) - zk);
-          cols.sk[tok] = cur.is ? cur.sk * a.scale_log2 : 0.0f;
-          cols.lv[tok] = cur.is ? lv : -INFINITY;
-          cols.rsv[tok] = cur.is ? exp2_fast(-lv) : 0.0f;
-          cols.rk[tok] = cur.is ? rk : 0.0f;
-          cols.rv[tok] = cur.is ? rv : 0.0f;
-          const bool any = __any_sync(0xffffffffu, cur.is && (rk != 0.0f || rv != 0.0f));
+          const float lv = fminf(fmaxf(__log2f(num.sv), -40.0f), 40.0f);
+          const float rv = none ? NAN : zero ? 0.0f : static_cast<float>(static_cast<int64_t>(num.zv) - zv);
+          const float rk = static_cast<float>(static_cast<int64_t>(num.zk) - zk);
+          cols.sk[tok] = is ? num.sk * a.scale_log2 : 0.0f;
+          cols.lv[tok] = is ? lv : -INFINITY;
+          cols.rsv[tok] = is ? exp2_fast(-lv) : 0.0f;
+          cols.rk[tok] = is ? rk : 0.0f;
+          cols.rv[tok] = is ? rv : 0.0f;
+          const bool any = __any_sync(0xffffffffu, is && (rk != 0.0f || rv != 0.0f));
           if (lane == 0) cols.rest[tok >> 5] = any;
         }
-        auto unpack = [&](const uint32_t* w, int32_t z, bool blank, uint8_t* tile) {
-          const __half2 c1 = __half2half2(__int2half_rn(-1032 - z)), c0 = __half2half2(__int2half_rn(-72 - z));
-          const uint32_t z1024 = *reinterpret_cast<const uint32_t*>(&c1), z64 = *reinterpret_cast<const uint32_t*>(&c0);
-#pragma unroll
-          for (int i = 0; i < P::kWords; ++i) {
-            const uint32_t x = w[i], y = x >> 8;
-            uint4 e = make_uint4(add_half2(nib_1024(x), z1024), add_half2(nib_64(x), z64),
-                                 add_half2(nib_1024(y), z1024), add_half2(nib_64(y), z64));
-            if (blank) e = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(tile + tile_at(tok, half * P::kWords + i)) = e;
-          }
-        };
-        unpack(cur.k, zk, false, kt);
+        unpack(kw, zk, false, kt);
         fence_proxy_async_smem();
         mbar_arrive(&bars[kKFull + st]);
-        unpack(cur.x, zv, zero || !cur.is, vt);
+        if (j + 1 < it.take) {
+          load(0, next, kw);
+          num = numbers(next);
+        }
+        unpack(vw, zv, zero || !is, vt);
         fence_proxy_async_smem();
         mbar_arrive(&bars[kVFull + st]);
+        slot = next;
+        next = after;
       }
     } else if (lane == 0) {
       // ------------------------------------------------------------ MMA issue
@@ -482,7 +496,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
     if (*abort_flag) break;
   }
   __syncthreads();
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
 template <int D>

@@ -42,36 +42,55 @@ __device__ __forceinline__ int32_t seen(const SeqRows& r, int32_t i, int causal)
   return causal ? min(max(r.before + i + 1, 0), r.len) : r.len;
 }
 
+// (the caller holds here * gq below 2^31)
 __device__ __forceinline__ int32_t seq_tiles(const SplitPlan& p, const SeqRows& r) {
-  return static_cast<int32_t>((static_cast<int64_t>(r.here) * p.gq + p.rows - 1) / p.rows);
+  return static_cast<int32_t>((static_cast<uint32_t>(r.here) * p.gq + p.rows - 1) / static_cast<uint32_t>(p.rows));
 }
 
 // Tokens that a tile's last row sees, and its units (at least one: rows that see nothing are written too).
 __device__ __forceinline__ int32_t tile_seen(const SplitPlan& p, const SeqRows& r, int32_t tile) {
-  const int64_t last = min((static_cast<int64_t>(tile) + 1) * p.rows, static_cast<int64_t>(r.here) * p.gq) - 1;
-  return seen(r, static_cast<int32_t>(last / p.gq), p.causal);
+  if (!p.causal) return r.len;
+  const uint32_t rows = static_cast<uint32_t>(r.here) * p.gq;
+  const uint32_t last = min((static_cast<uint32_t>(tile) + 1) * p.rows, rows) - 1;
+  return seen(r, static_cast<int32_t>(last / static_cast<uint32_t>(p.gq)), 1);
 }
 __device__ __forceinline__ int32_t tile_units(const SplitPlan& p, const SeqRows& r, int32_t tile) {
-  return max((tile_seen(p, r, tile) + p.unit - 1) / p.unit, 1);
+  return max(static_cast<int32_t>((static_cast<uint32_t>(tile_seen(p, r, tile)) + p.unit - 1) /
+                                  static_cast<uint32_t>(p.unit)), 1);
 }
 
-// prefix[b] = units of the sequences before b, prefix[batch] = all.  Called by a whole block.
-template <int THREADS>
+// prefix[b] = units of the sequences before b, prefix[batch] = all.  Called by a whole block.  MANY: sequences have
+// many tiles, a warp adds up one's; else a thread does.
+template <int THREADS, bool MANY>
 __device__ __forceinline__ void split_prefix(const KvView& v, const SplitPlan& p, int64_t* prefix) {
   __shared__ int64_t warp_sum[THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (MANY) {
+    for (int32_t b = warp; b < v.batch; b += THREADS / 32) {
+      const SeqRows r = seq_rows(v, b);
+      const int32_t tiles = seq_tiles(p, r);
+      int64_t x = 0;
+      for (int32_t t = lane; t < tiles; t += 32) x += tile_units(p, r, t);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == 0) prefix[b + 1] = x * p.head_blocks;
+    }
+    __syncthreads();
+  }
   int64_t base = 0;
   if (threadIdx.x == 0) prefix[0] = 0;
   for (int32_t b0 = 0; b0 < v.batch; b0 += THREADS) {
     const int32_t b = b0 + threadIdx.x;
     int64_t x = 0;
     if (b < v.batch) {
-      const SeqRows r = seq_rows(v, b);
-      const int32_t tiles = seq_tiles(p, r);
-      if (!p.causal && tiles > 0) x = static_cast<int64_t>(tiles) * tile_units(p, r, 0);
-      else
+      if (MANY) {
+        x = prefix[b + 1];
+      } else {
+        const SeqRows r = seq_rows(v, b);
+        const int32_t tiles = seq_tiles(p, r);
         for (int32_t t = 0; t < tiles; ++t) x += tile_units(p, r, t);
-      x *= p.head_blocks;
+        x *= p.head_blocks;
+      }
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -47,7 +47,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 __device__ __forceinline__ float inverse_or_zero(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
 // The item that unit `at` belongs to, and how many of its units a block with `left` units ahead takes.  *b:
-// a sequence at or before the item's, which it becomes (the item's already unless SEARCH).
+// a sequence at or before the item's, which it becomes (the item's already unless SEARCH).  Called by whole warps.
 struct Item {
   SeqRows rows;
   int32_t tile, block, unit;                   // tile of rows, block of heads, first unit
@@ -65,13 +65,32 @@ __device__ __forceinline__ Item find_item(const KvView& v, const SplitPlan& p, c
   *b = lo;
   Item it;
   it.rows = seq_rows(v, lo);
+  // the tile: 32 of them at a time, one a lane
   int64_t off = at - prefix[lo];
-  it.tile = 0;
-  int32_t tu = tile_units(p, it.rows, 0);
-  while (off >= static_cast<int64_t>(tu) * p.head_blocks) {
-    off -= static_cast<int64_t>(tu) * p.head_blocks;
-    tu = tile_units(p, it.rows, ++it.tile);
+  int32_t tile = 0, tu = tile_units(p, it.rows, 0);
+  if (off >= static_cast<int64_t>(tu) * p.head_blocks) {
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const int32_t tiles = seq_tiles(p, it.rows);
+    for (int32_t t0 = 0;; t0 += 32) {
+      const int64_t mine = t0 + lane < tiles ? static_cast<int64_t>(tile_units(p, it.rows, t0 + lane)) * p.head_blocks : 0;
+      int64_t upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const uint32_t there = __ballot_sync(0xffffffffu, off < upto);
+      if (there != 0 || t0 + 32 >= tiles) {
+        const int at_lane = there != 0 ? __ffs(there) - 1 : 0;
+        tile = t0 + at_lane;
+        off -= __shfl_sync(0xffffffffu, upto - mine, at_lane);
+        break;
+      }
+      off -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    tu = tile_units(p, it.rows, tile);
   }
+  it.tile = tile;
   it.block = p.head_blocks == 1 ? 0 : static_cast<int32_t>(static_cast<uint32_t>(off) / static_cast<uint32_t>(tu));
   it.unit = static_cast<int32_t>(off - static_cast<int64_t>(it.block) * tu);
   it.take = min(tu - it.unit, left);

@@ -77,6 +77,8 @@ qr_status make_view(const qr_kv_cache* c, const qr_kv_seqs* s, int64_t tokens, b
 qr_status check_queries(const KvView& v, const uint16_t* Q, int64_t ldq, int32_t q_heads, float scale) {
   if (q_heads <= 0 || q_heads % v.heads != 0 || !std::isfinite(scale)) return QR_ERR_INVALID_ARG;
   if (static_cast<int64_t>(q_heads) * v.head_dim > 65536) return QR_ERR_UNSUPPORTED;
+  // query rows of a key head are counted in 32 bits
+  if (static_cast<int64_t>(v.tokens) * (q_heads / v.heads) > 0x7FFF0000) return QR_ERR_UNSUPPORTED;
   if (v.tokens > 0) {
     if (Q == nullptr || ldq < static_cast<int64_t>(q_heads) * v.head_dim) return QR_ERR_INVALID_ARG;
     if (!aligned<16>(Q) || ldq % 8 != 0) return QR_ERR_ALIGNMENT;
