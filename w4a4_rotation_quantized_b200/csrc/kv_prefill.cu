@@ -17,9 +17,11 @@
 // 13 warps (so that a thread may have 128 registers): two softmax warpgroups (one a tile), four warps that load and
 // unpack the next keys, one token a thread, one that issues the matrix instructions: while one tile is in its
 // softmax the tensor cores have the other.  Two tiles share an unpacked key tile.  The softmax goes over the
-// scores once, with the maximum of the keys before: only when a weight would pass 2^15 it goes back, finds the
-// new maximum, rescales and starts over (the weights wait in registers until then, the scores in tensor
-// memory).  Work is shared out and joined as in kv_split.cuh.
+// scores once, 32 columns at a time, with the maximum of the keys before: only when a weight of the columns at
+// hand would pass 2^15 is m raised, by a whole number, and what has been made with the old one (l, O, the weights
+// of this key tile) multiplied by that power of two.  The roles go through the block's items each on its own, so
+// that the next item's queries and first scores are there when the softmax has written the last one's
+// outputs.  Work is shared out and joined as in kv_split.cuh.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -65,7 +67,7 @@ struct Cols {
   }
 };
 
-enum Bar { kQFull = 0, kKFull = 1, kVFull = 3, kFree = 5, kSFull = 7, kPFull = 9, kODone = 11, kBars = 13 };
+enum Bar { kQFull = 0, kKFull = 1, kVFull = 3, kFree = 5, kSFull = 7, kPFull = 9, kODone = 11, kORead = 13, kBars = 15 };
 
 // Byte of the 16-byte chunk `chunk` (of 8 elements) of row r in a swizzled tile of 128 rows.
 __device__ __forceinline__ int tile_at(int r, int chunk) {
@@ -96,6 +98,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
       mbar_init(&bars[kSFull + i], 1);
       mbar_init(&bars[kPFull + i], kSoftmaxThreads);
       mbar_init(&bars[kODone + i], 1);
+      mbar_init(&bars[kORead + i], kSoftmaxThreads);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -126,47 +129,57 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
     return __all_sync(0xffffffffu, wait(bar, n, code));
   };
 
-  uint32_t steps = 0, segments = 0;              // key tiles and items so far
-  uint32_t tile_steps[2] = {0, 0};               // ... that tile 0 and 1 took part in
+  // what a role counts as it goes through the items: key tiles and items, of the block and of each query tile
+  struct Counts {
+    uint32_t steps, items, tile_steps[2], tile_items[2];
+    __device__ __forceinline__ void next(int32_t take, int tiles) {
+      steps += take;
+      ++items;
+      for (int t = 0; t < tiles; ++t) {
+        tile_steps[t] += take;
+        ++tile_items[t];
+      }
+    }
+  } n{};
+  auto tiles_of = [&](const Item& it) {
+    return P::kTiles == 2 && it.tile * a.plan.rows + 128 < it.rows.here * a.plan.gq ? 2 : 1;
+  };
+  bool ok = true;
   int32_t b = 0;
-  for (int32_t done = 0; done < count; ++segments) {
-    const Item it = find_item(v, a.plan, prefix, start + done, count - done, &b);
-    const SeqRows& rows = it.rows;
-    const int32_t row0 = it.tile * a.plan.rows, all_rows = rows.here * a.plan.gq;
-    const int tiles = P::kTiles == 2 && row0 + 128 < all_rows ? 2 : 1;
-    const int head = it.block;
-    const int32_t t_first = it.unit * kKeys;
-    bool ok = true;
 
-    if (warp < 8) {
-      // ------------------------------------------------------------- softmax
-      const int t = warp >> 2;
+  if (warp < 8) {
+    // --------------------------------------------------------------- softmax
+    const int t = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;            // 32 (warp & 3) in the lane field
+    const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + t * D;
+    const int r = 128 * t + (warp & 3) * 32 + lane;
+    for (int32_t done = 0; done < count && ok;) {
+      const Item it = find_item(v, a.plan, prefix, start + done, count - done, &b);
+      const int tiles = tiles_of(it);
       if (t < tiles) {
-        const int r = 128 * t + (warp & 3) * 32 + lane;
-        const int32_t rr = row0 + r;
-        const bool has = rr < all_rows;
-        const int32_t limit = has ? seen(rows, rr / a.plan.gq, a.plan.causal) : 0;
-        const int32_t all_limit = seen(rows, (row0 + 128 * t) / a.plan.gq, a.plan.causal);
-        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;        // 32 (warp & 3) in the lane field
-        const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + t * D;
-        const __half* q_row = has ? a.q + (rows.first + rr / a.plan.gq) * a.ldq +
-                                        static_cast<int64_t>(head * a.plan.gq + rr % a.plan.gq) * D : nullptr;
-        float m = 0.0f, l = 0.0f, zs = 0.0f, qsum = 0.0f;
+        const int32_t row0 = it.tile * a.plan.rows, rr = row0 + r;
+        const bool has = rr < it.rows.here * a.plan.gq;
+        const int32_t tok = has ? rr / a.plan.gq : 0, qh = it.block * a.plan.gq + (has ? rr % a.plan.gq : 0);
+        const int32_t limit = has ? seen(it.rows, tok, a.plan.causal) : 0;
+        const int32_t all_limit = seen(it.rows, (row0 + 128 * t) / a.plan.gq, a.plan.causal);
+        float m = 0.0f, zs = 0.0f, qsum = 0.0f;
+        uint64_t l2 = 0;
         bool started = !has, summed = false;               // (rows of nobody hold nothing up)
-        for (int32_t j = 0; j < it.take && ok; ++j) {
-          const uint32_t n = steps + j, nt = tile_steps[t] + j;
-          const int st = n % P::kStages;
-          ok = wait_warp(kKFull + st, n / P::kStages, kDevTimeoutEpilogue) && wait_warp(kSFull + t, nt, kDevTimeoutEpilogue);
+        for (int32_t j = 0; j < it.take; ++j) {
+          const uint32_t step = n.steps + j, nt = n.tile_steps[t] + j;
+          const int st = step % P::kStages;
+          ok = wait_warp(kKFull + st, step / P::kStages, kDevTimeoutEpilogue) && wait_warp(kSFull + t, nt, kDevTimeoutEpilogue);
           if (!ok) break;
           tc_fence_after();
           const Cols cols(cols_at + st * P::kCols);
-          const int32_t t0 = t_first + j * kKeys;
+          const int32_t t0 = (it.unit + j) * kKeys;
           const int4 rest4 = *reinterpret_cast<const int4*>(cols.rest);
           const bool rest = (rest4.x | rest4.y | rest4.z | rest4.w) != 0;
           const bool plain = t0 + kKeys <= all_limit && !rest;
-          if (rest && !summed) {                         // sum of the row's queries, for remainders of key zeros
+          if (rest && !summed) {                           // sum of the row's queries, for remainders of key zeros
             summed = true;
-            if (q_row != nullptr)
+            if (has) {
+              const __half* q_row = a.q + (it.rows.first + tok) * a.ldq + static_cast<int64_t>(qh) * D;
               for (int e = 0; e < D; e += 8) {
                 const uint4 x = *reinterpret_cast<const uint4*>(q_row + e);
                 const __half2* h = reinterpret_cast<const __half2*>(&x);
@@ -176,189 +189,185 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
                   qsum += f.x + f.y;
                 }
               }
+            }
           }
           const int32_t lim = limit - t0;
-          // y of four columns from their sums.  MODE 0: every row sees every key; 1: not so; 2: and zeros leave remainders
-          auto four = [&](auto mode, const uint32_t* s, int col, float (&y)[4]) {
-            constexpr int MODE = decltype(mode)::value;
-            const float4 sk = *reinterpret_cast<const float4*>(cols.sk + col);
-            const float4 lv = *reinterpret_cast<const float4*>(cols.lv + col);
-            uint64_t x0 = f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1]));
-            uint64_t x1 = f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3]));
-            if constexpr (MODE == 2) {
-              const float4 rk = *reinterpret_cast<const float4*>(cols.rk + col);
-              x0 = f2_fma(f2_pack(-rk.x, -rk.y), f2_pack(qsum, qsum), x0);
-              x1 = f2_fma(f2_pack(-rk.z, -rk.w), f2_pack(qsum, qsum), x1);
+          // raises m where a weight would pass 2^15 (and sets it where no key has been seen)
+          auto raise = [&](float top, int ch) -> bool {
+            const bool high = started && top > m + 15.0f;
+            const float up = high ? ceilf(top - m) : 0.0f, f = high ? exp2_fast(-up) : 1.0f;
+            if (high) m += up;
+            else if (!started && top != -INFINITY) {
+              m = top;
+              started = true;
             }
-            f2_unpack(f2_fma(x0, f2_pack(sk.x, sk.y), f2_pack(lv.x, lv.y)), y[0], y[1]);
-            f2_unpack(f2_fma(x1, f2_pack(sk.z, sk.w), f2_pack(lv.z, lv.w)), y[2], y[3]);
-            if constexpr (MODE > 0) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (col + i >= lim) y[i] = -INFINITY;
-            }
-          };
-          auto maximum = [&](auto mode) {
-            float top = -INFINITY;
+            if (!__any_sync(0xffffffffu, high)) return true;
+            const uint64_t f2 = f2_pack(f, f);
+            l2 = f2_mul(l2, f2);
+            zs *= f;
+            const __half2 fh = __float2half2_rn(f);
+            tmem_st_wait();
 #pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-              uint32_t s[32];
-              tmem_ld_32x32b_x32(s_at + 32 * ch, s);
+            for (int c = 0; c < ch; ++c) {                 // the weights of this key tile so far
+              uint32_t w[16];
+              tmem_ld_32x32b_x16(s_at + 16 * c, w);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float y[4];
-                four(mode, s + i, 32 * ch + i, y);
-                top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
+              for (int i = 0; i < 16; ++i) {
+                const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(w + i), fh);
+                w[i] = *reinterpret_cast<const uint32_t*>(&x);
               }
+              tmem_st_32x32b_x16(s_at + 16 * c, w);
             }
-            return has ? top : -INFINITY;
-          };
-          uint32_t w[64];
-          float dl, dz;                                    // what this step adds to l and zs
-          auto weights = [&](auto mode) {                  // returns the maximum
-            constexpr int MODE = decltype(mode)::value;
-            const uint64_t nm = f2_pack(-m, -m);
-            uint64_t l2 = 0, l3 = 0;
-            float top = -INFINITY;
-            dz = 0.0f;
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-              uint32_t s[32];
-              tmem_ld_32x32b_x32(s_at + 32 * ch, s);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float y[4];
-                const int col = 32 * ch + i;
-                four(mode, s + i, col, y);
-                top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
-                const float4 r = *reinterpret_cast<const float4*>(cols.rsv + col);
-                f2_unpack(f2_add(f2_pack(y[0], y[1]), nm), y[0], y[1]);
-                f2_unpack(f2_add(f2_pack(y[2], y[3]), nm), y[2], y[3]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = exp2_fast(y[k]);
-                l2 = f2_fma(f2_pack(y[0], y[1]), f2_pack(r.x, r.y), l2);
-                l3 = f2_fma(f2_pack(y[2], y[3]), f2_pack(r.z, r.w), l3);
-                if constexpr (MODE == 2) {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const float rv = cols.rv[col + k];
-                    if (rv != 0.0f && y[k] != 0.0f) dz = fmaf(y[k], rv, dz);   // (NaN for a scale that is none)
-                  }
-                }
-                const __half2 h0 = __floats2half2_rn(y[0], y[1]), h1 = __floats2half2_rn(y[2], y[3]);
-                w[col / 2] = *reinterpret_cast<const uint32_t*>(&h0);
-                w[col / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-              }
-            }
-            float l0, l1;
-            f2_unpack(f2_add(l2, l3), l0, l1);
-            dl = l0 + l1;
-            return has ? top : -INFINITY;
-          };
-          auto step = [&](auto mode) -> bool {
-            for (bool exact = __any_sync(0xffffffffu, !started);; exact = true) {
-              if (exact) {
-                const float top = maximum(mode);
-                const bool grows = started && top > m;
-                const float f = grows ? exp2_fast(m - top) : 1.0f;
-                if (grows || (!started && top != -INFINITY)) m = top;
-                started |= top != -INFINITY;
-                if (__any_sync(0xffffffffu, grows)) {      // (never at the item's first keys)
-                  l *= f;
-                  zs *= f;
-                  if (!wait_warp(kODone + t, nt - 1, kDevTimeoutEpilogue)) return false;   // O is complete up to here
-                  tc_fence_after();
+            if (j > 0) {
+              if (!wait_warp(kODone + t, nt - 1, kDevTimeoutEpilogue)) return false;       // O is complete up to here
+              tc_fence_after();
 #pragma unroll 1
-                  for (int ch = 0; ch < D / 32; ++ch) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(o_at + 32 * ch, o);
-                    tmem_ld_wait();
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(o_at + 32 * c, o);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    tmem_st_32x32b_x32(o_at + 32 * ch, o);
-                  }
-                  tmem_st_wait();
-                }
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st_32x32b_x32(o_at + 32 * c, o);
               }
-              const float top = weights(mode);
-              if (exact || !__any_sync(0xffffffffu, top > m + 15.0f)) break;
             }
+            tmem_st_wait();
             return true;
           };
-          ok = plain ? step(std::integral_constant<int, 0>{})
-                     : rest ? step(std::integral_constant<int, 2>{}) : step(std::integral_constant<int, 1>{});
-          if (!ok) break;
-          l += dl;
-          zs += dz;
+          // 32 columns.  MODE 0: every row sees every key; 1: not so; 2: and zeros leave remainders
+          auto chunk = [&](auto mode, uint32_t (&s)[32], int ch) -> bool {
+            constexpr int MODE = decltype(mode)::value;
+            float top = -INFINITY;
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch)                   // over columns that have been read
-            tmem_st_32x32b_x32(s_at + 32 * ch, *reinterpret_cast<const uint32_t(*)[32]>(w + 32 * ch));
+            for (int i = 0; i < 32; i += 4) {
+              const int col = 32 * ch + i;
+              const float4 sk = *reinterpret_cast<const float4*>(cols.sk + col);
+              const float4 lv = *reinterpret_cast<const float4*>(cols.lv + col);
+              uint64_t x0 = f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+              uint64_t x1 = f2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+              if constexpr (MODE == 2) {
+                const float4 rk = *reinterpret_cast<const float4*>(cols.rk + col);
+                x0 = f2_fma(f2_pack(-rk.x, -rk.y), f2_pack(qsum, qsum), x0);
+                x1 = f2_fma(f2_pack(-rk.z, -rk.w), f2_pack(qsum, qsum), x1);
+              }
+              float y[4];
+              f2_unpack(f2_fma(x0, f2_pack(sk.x, sk.y), f2_pack(lv.x, lv.y)), y[0], y[1]);
+              f2_unpack(f2_fma(x1, f2_pack(sk.z, sk.w), f2_pack(lv.z, lv.w)), y[2], y[3]);
+              if constexpr (MODE > 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (col + k >= lim) y[k] = -INFINITY;
+              }
+              top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s[i + k] = __float_as_uint(y[k]);
+            }
+            if (__any_sync(0xffffffffu, has && (!started || top > m + 15.0f)) && !raise(has ? top : -INFINITY, ch))
+              return false;
+            const uint64_t nm = f2_pack(-m, -m);
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const int col = 32 * ch + i;
+              const float4 rs = *reinterpret_cast<const float4*>(cols.rsv + col);
+              float y[4];
+              f2_unpack(f2_add(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), nm), y[0], y[1]);
+              f2_unpack(f2_add(f2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), nm), y[2], y[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) y[k] = exp2_fast(y[k]);
+              l2 = f2_fma(f2_pack(y[0], y[1]), f2_pack(rs.x, rs.y), l2);
+              l2 = f2_fma(f2_pack(y[2], y[3]), f2_pack(rs.z, rs.w), l2);
+              if constexpr (MODE == 2) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float rv = cols.rv[col + k];
+                  if (rv != 0.0f && y[k] != 0.0f) zs = fmaf(y[k], rv, zs);       // (NaN for a scale that is none)
+                }
+              }
+              const __half2 h0 = __floats2half2_rn(y[0], y[1]), h1 = __floats2half2_rn(y[2], y[3]);
+              w[i / 2] = *reinterpret_cast<const uint32_t*>(&h0);
+              w[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+            }
+            tmem_st_32x32b_x16(s_at + 16 * ch, w);         // over columns that have been read
+            return true;
+          };
+          auto step_of = [&](auto mode) -> bool {
+            uint32_t s0[32], s1[32];                       // the next columns are on their way meanwhile
+            tmem_ld_32x32b_x32(s_at, s0);
+            tmem_ld_wait();
+            tmem_ld_32x32b_x32(s_at + 32, s1);
+            if (!chunk(mode, s0, 0)) return false;
+            tmem_ld_wait();
+            tmem_ld_32x32b_x32(s_at + 64, s0);
+            if (!chunk(mode, s1, 1)) return false;
+            tmem_ld_wait();
+            tmem_ld_32x32b_x32(s_at + 96, s1);
+            if (!chunk(mode, s0, 2)) return false;
+            tmem_ld_wait();
+            return chunk(mode, s1, 3);
+          };
+          ok = plain ? step_of(std::integral_constant<int, 0>{})
+                     : rest ? step_of(std::integral_constant<int, 2>{}) : step_of(std::integral_constant<int, 1>{});
+          if (!ok) break;
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&bars[kPFull + t]);
         }
-        if (ok) ok = wait_warp(kODone + t, tile_steps[t] + it.take - 1, kDevTimeoutEpilogue);
-        if (ok) {
-          tc_fence_after();
-          const int64_t token = rows.first + rr / a.plan.gq;
-          const int h = head * a.plan.gq + rr % a.plan.gq;
-          const int64_t part = part_at(a, blockIdx.x, done == 0 ? 0 : 1, 0, r);
-          const float inv = it.whole ? inverse_or_zero(l) : 1.0f;
+        if (ok) ok = wait_warp(kODone + t, n.tile_steps[t] + it.take - 1, kDevTimeoutEpilogue);
+        if (!ok) break;
+        tc_fence_after();
+        float l, l1;
+        f2_unpack(l2, l, l1);
+        l += l1;
+        const int64_t token = it.rows.first + tok, part = part_at(a, blockIdx.x, done == 0 ? 0 : 1, 0, r);
+        const float inv = it.whole ? inverse_or_zero(l) : 1.0f;
+        __half* out = a.out + token * a.ldo + qh * D;
 #pragma unroll 1
-          for (int ch = 0; ch < D / 32; ++ch) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(o_at + 32 * ch, o);
-            tmem_ld_wait();
-            if (!has) continue;
-            // columns of a chunk of 8 hold elements 0 4 1 5 2 6 3 7
-            float y[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              y[i] = (__uint_as_float(o[(i & 24) + ((i & 3) << 1) + ((i >> 2) & 1)]) - zs) * inv;
-            if (it.whole) {
-              store_half<32>(a.out + token * a.ldo + h * D + 32 * ch, y);
-            } else {
-              float4* to = reinterpret_cast<float4*>(a.part_o + part * D + 32 * ch);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) to[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-            }
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(o_at + 32 * ch, o);
+          tmem_ld_wait();
+          if (ch == D / 32 - 1) {                          // O may be written again
+            tc_fence_before();
+            mbar_arrive(&bars[kORead + t]);
           }
-          if (has) {
-            if (!it.whole) a.part_ml[part] = make_float2(m, l);
-            else if (a.lse != nullptr) a.lse[token * a.q_heads + h] = row_lse(m, l);
+          if (!has) continue;
+          // columns of a chunk of 8 hold elements 0 4 1 5 2 6 3 7
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            y[i] = (__uint_as_float(o[(i & 24) + ((i & 3) << 1) + ((i >> 2) & 1)]) - zs) * inv;
+          if (it.whole) {
+            store_half<32>(out + 32 * ch, y);
+          } else {
+            float4* to = reinterpret_cast<float4*>(a.part_o + part * D + 32 * ch);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) to[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
           }
         }
-      }
-      tc_fence_before();
-    } else if (warp < 12) {
-      // ------------------------------------------------- queries, keys, values
-      const int tok = tid - 2 * kSoftmaxThreads;
-      // queries: row tok of each tile; elements of a chunk in the order 0 4 1 5 2 6 3 7
-      for (int t = 0; t < tiles; ++t) {
-        const int32_t rr = row0 + 128 * t + tok;
-        const __half* from = rr < all_rows ? a.q + (rows.first + rr / a.plan.gq) * a.ldq +
-                                                 static_cast<int64_t>(head * a.plan.gq + rr % a.plan.gq) * D : nullptr;
-#pragma unroll 8
-        for (int chunk = 0; chunk < D / 8; ++chunk) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (from != nullptr) x = *reinterpret_cast<const uint4*>(from + chunk * 8);
-          *reinterpret_cast<uint4*>(q_tile + t * P::kTile + tile_at(tok, chunk)) =
-              make_uint4(byte_perm(x.x, x.z, 0x5410), byte_perm(x.x, x.z, 0x7632), byte_perm(x.y, x.w, 0x5410),
-                         byte_perm(x.y, x.w, 0x7632));
+        if (has) {
+          if (!it.whole) a.part_ml[part] = make_float2(m, l);
+          else if (a.lse != nullptr) a.lse[token * a.q_heads + qh] = row_lse(m, l);
         }
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&bars[kQFull]);
-
+      n.next(it.take, tiles);
+      done += it.take;
+    }
+  } else if (warp < 12) {
+    // --------------------------------------------------- queries, keys, values
+    const int tok = tid - 2 * kSoftmaxThreads;
+    constexpr int W = P::kWords;
+    const int64_t row_bytes = v.width >> 1;
+    for (int32_t done = 0; done < count && ok;) {
+      const Item it = find_item(v, a.plan, prefix, start + done, count - done, &b);
+      const int tiles = tiles_of(it);
+      const int head = it.block;
       // one token a thread: its key's codes are loaded a step ahead, its value's while the key is unpacked
-      constexpr int W = P::kWords;
-      const int64_t row_bytes = v.width >> 1;
       const int at = head * (D / 2);
       const uint32_t group = head * D / v.group;
       auto slot_of = [&](int32_t j) -> int64_t {
-        const int32_t t = t_first + j * kKeys + tok;
+        const int32_t t = (it.unit + j) * kKeys + tok;
         return j < it.take && t < it.seen ? kv_slot(v, v.table, b, t) : -1;
       };
       auto load = [&](int side, int64_t slot, uint32_t (&x)[W]) {
@@ -405,12 +414,34 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
       int64_t slot = slot_of(0), next = slot_of(1);
       load(0, slot, kw);
       Numbers num = numbers(slot);
-      for (int32_t j = 0; j < it.take && ok; ++j) {
-        const uint32_t n = steps + j;
-        const int st = n % P::kStages;
+      // queries: row tok of each tile; elements of a chunk in the order 0 4 1 5 2 6 3 7.  The tile of the item
+      // before has met its last keys when these scores are there.
+      for (int t = 0; t < tiles && ok; ++t) {
+        if (n.tile_steps[t] > 0) ok = wait_warp(kSFull + t, n.tile_steps[t] - 1, kDevTimeoutProducer);
+        if (!ok) break;
+        const int32_t rr = it.tile * a.plan.rows + 128 * t + tok;
+        const __half* from = rr < it.rows.here * a.plan.gq
+                                 ? a.q + (it.rows.first + rr / a.plan.gq) * a.ldq +
+                                       static_cast<int64_t>(head * a.plan.gq + rr % a.plan.gq) * D
+                                 : nullptr;
+#pragma unroll 8
+        for (int chunk = 0; chunk < D / 8; ++chunk) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (from != nullptr) x = *reinterpret_cast<const uint4*>(from + chunk * 8);
+          *reinterpret_cast<uint4*>(q_tile + t * P::kTile + tile_at(tok, chunk)) =
+              make_uint4(byte_perm(x.x, x.z, 0x5410), byte_perm(x.x, x.z, 0x7632), byte_perm(x.y, x.w, 0x5410),
+                         byte_perm(x.y, x.w, 0x7632));
+        }
+      }
+      if (!ok) break;
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[kQFull]);
+      for (int32_t j = 0; j < it.take; ++j) {
+        const uint32_t step = n.steps + j;
+        const int st = step % P::kStages;
         load(1, slot, vw);
         const int64_t after = slot_of(j + 2);
-        if (n >= P::kStages) ok = wait_warp(kFree + st, n / P::kStages - 1, kDevTimeoutProducer);
+        if (step >= P::kStages) ok = wait_warp(kFree + st, step / P::kStages - 1, kDevTimeoutProducer);
         if (!ok) break;
         uint8_t* kt = kv_tile + st * P::kStage;
         uint8_t* vt = kt + P::kTile;
@@ -443,59 +474,68 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
         slot = next;
         next = after;
       }
-    } else if (lane == 0) {
-      // ------------------------------------------------------------ MMA issue
-      constexpr uint32_t kIdescS = idesc_f16(kKeys);
-      constexpr uint32_t kIdescO = idesc_f16(D) | (1u << 16);          // B with N contiguous
-      const uint32_t q0 = smem_u32(q_tile), kv0 = smem_u32(kv_tile);
-      auto scores = [&](int t, int st) {
+      n.next(it.take, tiles);
+      done += it.take;
+    }
+  } else {
+    // -------------------------------------------------------------- MMA issue
+    constexpr uint32_t kIdescS = idesc_f16(kKeys);
+    constexpr uint32_t kIdescO = idesc_f16(D) | (1u << 16);            // B with N contiguous
+    const uint32_t q0 = smem_u32(q_tile), kv0 = smem_u32(kv_tile);
+    for (int32_t done = 0; done < count && ok;) {
+      const Item it = find_item(v, a.plan, prefix, start + done, count - done, &b);
+      const int tiles = tiles_of(it);
+      if (lane == 0) {
+        auto scores = [&](int t, int st) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_f16(tmem + 128 * t, smem_desc_kmajor(q0 + t * P::kTile + off, 128),
-                  smem_desc_kmajor(kv0 + st * P::kStage + off, 128), kIdescS, k > 0);
-        }
-        mma_commit(&bars[kSFull + t]);
-      };
-      ok = wait(kQFull, segments, kDevTimeoutMma) &&
-           wait(kKFull + steps % P::kStages, steps / P::kStages, kDevTimeoutMma);
-      if (ok) {
-        tc_fence_after();
-        for (int t = 0; t < tiles; ++t) scores(t, steps % P::kStages);
-      }
-      for (int32_t j = 0; j < it.take && ok; ++j) {
-        const uint32_t n = steps + j;
-        const int st = n % P::kStages;
-        ok = wait(kVFull + st, n / P::kStages, kDevTimeoutMma);
-        for (int t = 0; t < tiles && ok; ++t) {
-          if (!(ok = wait(kPFull + t, tile_steps[t] + j, kDevTimeoutMma))) break;
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+            mma_f16(tmem + 128 * t, smem_desc_kmajor(q0 + t * P::kTile + off, 128),
+                    smem_desc_kmajor(kv0 + st * P::kStage + off, 128), kIdescS, k > 0);
+          }
+          mma_commit(&bars[kSFull + t]);
+        };
+        ok = wait(kQFull, n.items, kDevTimeoutMma) &&
+             wait(kKFull + n.steps % P::kStages, n.steps / P::kStages, kDevTimeoutMma);
+        if (ok) {
           tc_fence_after();
+          for (int t = 0; t < tiles; ++t) scores(t, n.steps % P::kStages);
+        }
+        for (int32_t j = 0; j < it.take && ok; ++j) {
+          const uint32_t step = n.steps + j;
+          const int st = step % P::kStages;
+          ok = wait(kVFull + st, step / P::kStages, kDevTimeoutMma);
+          for (int t = 0; t < tiles && ok; ++t) {
+            ok = wait(kPFull + t, n.tile_steps[t] + j, kDevTimeoutMma);
+            // the outputs of the item before have been read
+            if (ok && j == 0 && n.tile_items[t] > 0) ok = wait(kORead + t, n.tile_items[t] - 1, kDevTimeoutMma);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)
-            mma_f16_ts(tmem + 256 + t * D, tmem + 128 * t + 8 * s,
-                       smem_desc_mn_sw128(kv0 + st * P::kStage + P::kTile + 2048 * s, 16384), kIdescO,
-                       j > 0 || s > 0);
-          mma_commit(&bars[kODone + t]);
-          if (t == tiles - 1) mma_commit(&bars[kFree + st]);
-          if (j + 1 < it.take) {
-            if (t == 0) {
-              if (!(ok = wait(kKFull + (n + 1) % P::kStages, (n + 1) / P::kStages, kDevTimeoutMma))) break;
-              tc_fence_after();
+            for (int s = 0; s < kKeys / 16; ++s)
+              mma_f16_ts(tmem + 256 + t * D, tmem + 128 * t + 8 * s,
+                         smem_desc_mn_sw128(kv0 + st * P::kStage + P::kTile + 2048 * s, 16384), kIdescO,
+                         j > 0 || s > 0);
+            mma_commit(&bars[kODone + t]);
+            if (t == tiles - 1) mma_commit(&bars[kFree + st]);
+            if (j + 1 < it.take) {
+              if (t == 0) {
+                if (!(ok = wait(kKFull + (step + 1) % P::kStages, (step + 1) / P::kStages, kDevTimeoutMma))) break;
+                tc_fence_after();
+              }
+              scores(t, (step + 1) % P::kStages);
             }
-            scores(t, (n + 1) % P::kStages);
           }
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
+      n.next(it.take, tiles);
+      done += it.take;
     }
-    steps += it.take;
-    tile_steps[0] += it.take;
-    if (tiles == 2) tile_steps[1] += it.take;
-    done += it.take;
-    __syncthreads();
-    tc_fence_after();
-    if (*abort_flag) break;
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
