@@ -4,7 +4,7 @@
 //
 // A block takes one key head and two tiles of 128 query rows (token, head of the group; one tile where a head
 // is 256 wide) over a range of keys, 128 at a time:
-//   S = Q K^T     tcgen05, both operands in shared memory, 128 x 128 fp32 in tensor memory
+//   S = Q K^T     tcgen05, both operands in shared memory, 128 x 64 fp32 in tensor memory, twice
 //   W = 2^(y - m) softmax warps, one row a thread, written back over S as fp16
 //   O += W V      tcgen05, W from tensor memory, V rows as they stand (MN-major), O in tensor memory
 // Codes become fp16 operands in shared memory as the whole numbers c - z, exact (kv_mma.cuh); the scales stay out
@@ -21,7 +21,8 @@
 // hand would pass 2^15 is m raised, by a whole number, and what has been made with the old one (l, O, the weights
 // of this key tile) multiplied by that power of two.  The roles go through the block's items each on its own, so
 // that the next item's queries and first scores are there when the softmax has written the last one's
-// outputs.  Work is shared out and joined as in kv_split.cuh.
+// outputs.  Scores come 64 keys at a time into two places a tile, so that the next ones are there when the softmax has
+// done with the last.  Work is shared out and joined as in kv_split.cuh.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -67,7 +68,10 @@ struct Cols {
   }
 };
 
-enum Bar { kQFull = 0, kKFull = 1, kVFull = 3, kFree = 5, kSFull = 7, kPFull = 9, kODone = 11, kORead = 13, kBars = 15 };
+// A wait names the completion it wants by its parity, so it must come when the one before is known to be over:
+// kSFull, kPFull and kODone have a barrier for each place of a tile (2 t + place), since the products of one
+// place may still run when the other's are waited for.
+enum Bar { kQFull = 0, kKFull = 1, kVFull = 3, kFree = 5, kSFull = 7, kPFull = 11, kODone = 15, kORead = 19, kQFree = 21, kBars = 22 };
 
 // Byte of the 16-byte chunk `chunk` (of 8 elements) of row r in a swizzled tile of 128 rows.
 __device__ __forceinline__ int tile_at(int r, int chunk) {
@@ -91,13 +95,16 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
 
   if (tid == 0) {
     mbar_init(&bars[kQFull], kUnpackThreads);
+    mbar_init(&bars[kQFree], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[kKFull + i], kUnpackThreads);
       mbar_init(&bars[kVFull + i], kUnpackThreads);
       mbar_init(&bars[kFree + i], 1);
-      mbar_init(&bars[kSFull + i], 1);
-      mbar_init(&bars[kPFull + i], kSoftmaxThreads);
-      mbar_init(&bars[kODone + i], 1);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&bars[kSFull + 2 * k + i], 1);
+        mbar_init(&bars[kODone + 2 * k + i], 1);
+        mbar_init(&bars[kPFull + 2 * k + i], kSoftmaxThreads);
+      }
       mbar_init(&bars[kORead + i], kSoftmaxThreads);
     }
     *abort_flag = 0;
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
     // --------------------------------------------------------------- softmax
     const int t = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;            // 32 (warp & 3) in the lane field
-    const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + t * D;
+    const uint32_t o_at = tmem + lanes + 256 + t * D;
     const int r = 128 * t + (warp & 3) * 32 + lane;
     for (int32_t done = 0; done < count && ok;) {
       const Item it = find_item(v, a.plan, prefix, start + done, count - done, &b);
@@ -165,17 +172,20 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
         float m = 0.0f, zs = 0.0f, qsum = 0.0f;
         uint64_t l2 = 0;
         bool started = !has, summed = false;               // (rows of nobody hold nothing up)
-        for (int32_t j = 0; j < it.take; ++j) {
-          const uint32_t step = n.steps + j, nt = n.tile_steps[t] + j;
-          const int st = step % P::kStages;
-          ok = wait_warp(kKFull + st, step / P::kStages, kDevTimeoutEpilogue) && wait_warp(kSFull + t, nt, kDevTimeoutEpilogue);
+        for (int32_t j = 0; j < 2 * it.take; ++j) {
+          const uint32_t step = n.steps + (j >> 1), nt = 2 * n.tile_steps[t] + j;     // j, nt: 64 keys at a time
+          const int st = step % P::kStages, place = j & 1;
+          const uint32_t s_at = tmem + lanes + 128 * t + 64 * place;
+          ok = wait_warp(kSFull + 2 * t + place, nt >> 1, kDevTimeoutEpilogue) &&
+               wait_warp(kKFull + st, step / P::kStages, kDevTimeoutEpilogue);      // (has been: to see its numbers)
           if (!ok) break;
           tc_fence_after();
           const Cols cols(cols_at + st * P::kCols);
-          const int32_t t0 = (it.unit + j) * kKeys;
+          const int32_t t0 = it.unit * kKeys + j * 64;
+          const int col0 = 64 * place;
           const int4 rest4 = *reinterpret_cast<const int4*>(cols.rest);
           const bool rest = (rest4.x | rest4.y | rest4.z | rest4.w) != 0;
-          const bool plain = t0 + kKeys <= all_limit && !rest;
+          const bool plain = t0 + 64 <= all_limit && !rest;
           if (rest && !summed) {                           // sum of the row's queries, for remainders of key zeros
             summed = true;
             if (has) {
@@ -220,7 +230,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
               tmem_st_32x32b_x16(s_at + 16 * c, w);
             }
             if (j > 0) {
-              if (!wait_warp(kODone + t, nt - 1, kDevTimeoutEpilogue)) return false;       // O is complete up to here
+              if (!wait_warp(kODone + 2 * t + 1 - place, (nt - 1) >> 1, kDevTimeoutEpilogue)) return false;   // O is complete up to here
               tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const int col = 32 * ch + i;
+              const int col = col0 + 32 * ch + i;
               const float4 sk = *reinterpret_cast<const float4*>(cols.sk + col);
               const float4 lv = *reinterpret_cast<const float4*>(cols.lv + col);
               uint64_t x0 = f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
@@ -257,7 +267,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
               if constexpr (MODE > 0) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  if (col + k >= lim) y[k] = -INFINITY;
+                  if (32 * ch + i + k >= lim) y[k] = -INFINITY;
               }
               top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
 #pragma unroll
@@ -269,7 +279,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const int col = 32 * ch + i;
+              const int col = col0 + 32 * ch + i;
               const float4 rs = *reinterpret_cast<const float4*>(cols.rsv + col);
               float y[4];
               f2_unpack(f2_add(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), nm), y[0], y[1]);
@@ -299,22 +309,16 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
             tmem_ld_32x32b_x32(s_at + 32, s1);
             if (!chunk(mode, s0, 0)) return false;
             tmem_ld_wait();
-            tmem_ld_32x32b_x32(s_at + 64, s0);
-            if (!chunk(mode, s1, 1)) return false;
-            tmem_ld_wait();
-            tmem_ld_32x32b_x32(s_at + 96, s1);
-            if (!chunk(mode, s0, 2)) return false;
-            tmem_ld_wait();
-            return chunk(mode, s1, 3);
+            return chunk(mode, s1, 1);
           };
           ok = plain ? step_of(std::integral_constant<int, 0>{})
                      : rest ? step_of(std::integral_constant<int, 2>{}) : step_of(std::integral_constant<int, 1>{});
           if (!ok) break;
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(&bars[kPFull + t]);
+          mbar_arrive(&bars[kPFull + 2 * t + place]);
         }
-        if (ok) ok = wait_warp(kODone + t, n.tile_steps[t] + it.take - 1, kDevTimeoutEpilogue);
+        if (ok) ok = wait_warp(kODone + 2 * t + 1, n.tile_steps[t] + it.take - 1, kDevTimeoutEpilogue);
         if (!ok) break;
         tc_fence_after();
         float l, l1;
@@ -414,11 +418,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
       int64_t slot = slot_of(0), next = slot_of(1);
       load(0, slot, kw);
       Numbers num = numbers(slot);
-      // queries: row tok of each tile; elements of a chunk in the order 0 4 1 5 2 6 3 7.  The tile of the item
-      // before has met its last keys when these scores are there.
-      for (int t = 0; t < tiles && ok; ++t) {
-        if (n.tile_steps[t] > 0) ok = wait_warp(kSFull + t, n.tile_steps[t] - 1, kDevTimeoutProducer);
-        if (!ok) break;
+      // queries: row tok of each tile; elements of a chunk in the order 0 4 1 5 2 6 3 7.  Those of the item before
+      // have met their last keys.
+      if (n.items > 0) ok = wait_warp(kQFree, n.items - 1, kDevTimeoutProducer);
+      if (!ok) break;
+      for (int t = 0; t < tiles; ++t) {
         const int32_t rr = it.tile * a.plan.rows + 128 * t + tok;
         const __half* from = rr < it.rows.here * a.plan.gq
                                  ? a.q + (it.rows.first + rr / a.plan.gq) * a.ldq +
@@ -433,7 +437,6 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
                          byte_perm(x.y, x.w, 0x7632));
         }
       }
-      if (!ok) break;
       fence_proxy_async_smem();
       mbar_arrive(&bars[kQFull]);
       for (int32_t j = 0; j < it.take; ++j) {
@@ -479,51 +482,57 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
     }
   } else {
     // -------------------------------------------------------------- MMA issue
-    constexpr uint32_t kIdescS = idesc_f16(kKeys);
+    constexpr uint32_t kIdescS = idesc_f16(64);
     constexpr uint32_t kIdescO = idesc_f16(D) | (1u << 16);            // B with N contiguous
     const uint32_t q0 = smem_u32(q_tile), kv0 = smem_u32(kv_tile);
     for (int32_t done = 0; done < count && ok;) {
       const Item it = find_item(v, a.plan, prefix, start + done, count - done, &b);
       const int tiles = tiles_of(it);
       if (lane == 0) {
-        auto scores = [&](int t, int st) {
+        // scores of tile t with 64 keys: half `place` of stage st
+        auto scores = [&](int t, int st, int place) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-            mma_f16(tmem + 128 * t, smem_desc_kmajor(q0 + t * P::kTile + off, 128),
-                    smem_desc_kmajor(kv0 + st * P::kStage + off, 128), kIdescS, k > 0);
+            mma_f16(tmem + 128 * t + 64 * place, smem_desc_kmajor(q0 + t * P::kTile + off, 128),
+                    smem_desc_kmajor(kv0 + st * P::kStage + off + place * 8192, 128), kIdescS, k > 0);
           }
-          mma_commit(&bars[kSFull + t]);
+          mma_commit(&bars[kSFull + 2 * t + place]);
         };
-        ok = wait(kQFull, n.items, kDevTimeoutMma) &&
-             wait(kKFull + n.steps % P::kStages, n.steps / P::kStages, kDevTimeoutMma);
-        if (ok) {
-          tc_fence_after();
-          for (int t = 0; t < tiles; ++t) scores(t, n.steps % P::kStages);
-        }
-        for (int32_t j = 0; j < it.take && ok; ++j) {
-          const uint32_t step = n.steps + j;
-          const int st = step % P::kStages;
-          ok = wait(kVFull + st, step / P::kStages, kDevTimeoutMma);
+        auto wait_keys = [&](uint32_t step) {
+          const bool there = wait(kKFull + step % P::kStages, step / P::kStages, kDevTimeoutMma);
+          if (there) tc_fence_after();
+          return there;
+        };
+        ok = wait(kQFull, n.items, kDevTimeoutMma) && wait_keys(n.steps);
+        for (int place = 0; place < 2 && ok; ++place)
+          for (int t = 0; t < tiles; ++t) scores(t, n.steps % P::kStages, place);
+        if (ok && it.take == 1) mma_commit(&bars[kQFree]);
+        for (int32_t j = 0; j < 2 * it.take && ok; ++j) {
+          const uint32_t step = n.steps + (j >> 1);
+          const int st = step % P::kStages, place = j & 1;
+          if (place == 0) ok = wait(kVFull + st, step / P::kStages, kDevTimeoutMma);
           for (int t = 0; t < tiles && ok; ++t) {
-            ok = wait(kPFull + t, n.tile_steps[t] + j, kDevTimeoutMma);
+            ok = wait(kPFull + 2 * t + place, n.tile_steps[t] + (j >> 1), kDevTimeoutMma);
             // the outputs of the item before have been read
             if (ok && j == 0 && n.tile_items[t] > 0) ok = wait(kORead + t, n.tile_items[t] - 1, kDevTimeoutMma);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int s = 0; s < kKeys / 16; ++s)
-              mma_f16_ts(tmem + 256 + t * D, tmem + 128 * t + 8 * s,
-                         smem_desc_mn_sw128(kv0 + st * P::kStage + P::kTile + 2048 * s, 16384), kIdescO,
+            for (int s = 0; s < 4; ++s)
+              mma_f16_ts(tmem + 256 + t * D, tmem + 128 * t + 64 * place + 8 * s,
+                         smem_desc_mn_sw128(kv0 + st * P::kStage + P::kTile + 2048 * (4 * place + s), 16384), kIdescO,
                          j > 0 || s > 0);
-            mma_commit(&bars[kODone + t]);
-            if (t == tiles - 1) mma_commit(&bars[kFree + st]);
-            if (j + 1 < it.take) {
-              if (t == 0) {
-                if (!(ok = wait(kKFull + (step + 1) % P::kStages, (step + 1) / P::kStages, kDevTimeoutMma))) break;
-                tc_fence_after();
-              }
-              scores(t, (step + 1) % P::kStages);
+            mma_commit(&bars[kODone + 2 * t + place]);
+            if (t == tiles - 1 && place == 1) mma_commit(&bars[kFree + st]);
+            // the same half of the next keys, into the place that these products have left (with one stage, both
+            // halves when the stage is free)
+            const bool more = j + 2 < 2 * it.take + (P::kStages == 1 ? 1 : 0);
+            if (more && (P::kStages > 1 || place == 1)) {
+              if (t == 0 && (P::kStages == 1 || place == 0) && !(ok = wait_keys(step + 1))) break;
+              if (P::kStages == 1) scores(t, 0, 0);
+              scores(t, (step + 1) % P::kStages, place);
+              if (t == tiles - 1 && place == 1 && (j >> 1) + 2 == it.take) mma_commit(&bars[kQFree]);
             }
           }
         }
