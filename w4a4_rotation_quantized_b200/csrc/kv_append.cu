@@ -7,20 +7,17 @@
 // butterfly's additions are those of kv_group_quant_kernel, so that without a rope
 // both give the same bits.
 //
-// Memory-bound: 2 (H_q + 2 H_k) d bytes read and 2 H_q d + H_k (d + 16 d / g) written
-// a token.  One warp takes one group of 32 E consecutive values of a row (whole
-// heads) at a time, lane L elements [E L, E L + E): vector loads and stores, the
-// butterflies in registers and by shuffles.  A rope turns (i, i + pairs): the
-// lane reads its elements' partners from memory a second time (they are in
-// L1, since another lane of the warp just asked for them), which is cheaper to
-// address than a shuffle whose distance depends on the number of pairs.  The angles
-// depend on the token alone, not on the head: a block forms the sines and cosines of
-// its tokens once, in double precision (positions pass 2^17 radians, where a
-// float32 product is off by more than the last bits of the codes), and its warps
-// share them through shared memory.
+// 2 (H_q + 2 H_k) d bytes read and 2 H_q d + H_k (d + 16 d / g) written a token, against some 14 operations an
+// element: a lane holds 16 consecutive elements, so that four of the butterfly's stages run in registers (on
+// pairs of fp32) and only those above them by shuffles (4 elements a lane: 276 us for 6200 tokens of 32 + 2 x 32
+// heads; the issue of 250 instructions for 128 elements bound it).  A rope turns (i, i + pairs): the lane reads
+// its elements' partners from memory a second time (they are in L1, since another lane just asked for them), which
+// is cheaper to address than shuffles whose distance depends on the number of pairs.  The angles depend on the
+// token alone, not on the head: a block forms the sines and cosines of its tokens once, in double precision
+// (positions pass 2^17 radians, where a float32 product is off by more than the last bits of the codes), and its
+// warps share them through shared memory.
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "kv_device.cuh"
 #include "qr_internal.h"
@@ -50,29 +47,27 @@ struct AppendArgs {
   float inv_sqrt;
 };
 
-// Where the elements of a rope meet: the partner of element h of a head, and its pair;
-// pair < 0 when h is not turned.
-__device__ __forceinline__ int rope_pair(const AppendArgs& a, int h, int* partner, bool* second) {
-  if (h >= 2 * a.pairs) return -1;
-  if (a.interleaved) {
-    *partner = h ^ 1;
-    *second = h & 1;
-    return h >> 1;
+constexpr int kLane = 16;                 // elements of a lane
+
+// 16 consecutive fp16 values as fp32.
+__device__ __forceinline__ void load_16(const __half* p, float (&x)[kLane]) {
+  uint4 raw[2];
+  raw[0] = reinterpret_cast<const uint4*>(p)[0];
+  raw[1] = reinterpret_cast<const uint4*>(p)[1];
+  const __half2* h = reinterpret_cast<const __half2*>(raw);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __half22float2(h[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
   }
-  *second = h >= a.pairs;
-  *partner = *second ? h - a.pairs : h + a.pairs;
-  return *second ? h - a.pairs : h;
 }
 
-template <int E>
-__global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const AppendArgs a) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int G = 32 * E;
-  constexpr int LE = E == 4 ? 2 : 3;
-  using V = typename std::conditional<E == 4, uint2, uint4>::type;
-  using C = typename std::conditional<E == 4, uint16_t, uint32_t>::type;
-  __shared__ float2 turn[kTokensPerBlock][kMaxPairs];       // (cos, sin)
+  // of the block's tokens: cosines, sines and sines with the other sign
+  __shared__ __align__(16) float turn[kTokensPerBlock][3][kMaxPairs];
   __shared__ int32_t token_seq[kTokensPerBlock];
   __shared__ int64_t token_slot[kTokensPerBlock];           // -1: no place for k and v
   const KvView& v = a.v;
@@ -108,127 +103,132 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(AppendArgs
       if (ax >= 0 && ax < a.axes)
         sincos(static_cast<double>(a.positions[ax * a.ld_pos + i0 + u]) *
                    static_cast<double>(a.inv_freq[j]), &s, &c);
-      turn[u][j] = make_float2(static_cast<float>(c), static_cast<float>(s));
+      turn[u][0][j] = static_cast<float>(c);
+      turn[u][1][j] = static_cast<float>(s);
+      turn[u][2][j] = -static_cast<float>(s);
     }
   }
   __syncthreads();
 
-  const int per_token = a.jobs[0] + a.jobs[1] + a.jobs[2];
-  const int stride = gridDim.y * kAppendWarps;
+  const int lanes = v.group / kLane, per = 32 / lanes;      // lanes of a group, groups of a warp
+  const int lg = lane / lanes, in_group = lane % lanes * kLane;
+  const int jobs_of[3] = {(a.jobs[0] + per - 1) / per, (a.jobs[1] + per - 1) / per, (a.jobs[2] + per - 1) / per};
+  const int per_token = jobs_of[0] + jobs_of[1] + jobs_of[2];
   const int jobs = kTokensPerBlock * per_token;
-  for (int job = blockIdx.y * kAppendWarps + warp; job < jobs; job += stride) {
+  for (int job = blockIdx.y * kAppendWarps + warp; job < jobs; job += gridDim.y * kAppendWarps) {
     const int u = job / per_token;
     int g = job - u * per_token;
     const int32_t i = i0 + u;
     if (i >= v.tokens || token_seq[u] >= v.batch) continue;      // uniform over the warp
-    const int side = g < a.jobs[0] ? 0 : g < a.jobs[0] + a.jobs[1] ? 1 : 2;
-    g -= side == 0 ? 0 : side == 1 ? a.jobs[0] : a.jobs[0] + a.jobs[1];
+    const int side = g < jobs_of[0] ? 0 : g < jobs_of[0] + jobs_of[1] ? 1 : 2;
+    g -= side == 0 ? 0 : side == 1 ? jobs_of[0] : jobs_of[0] + jobs_of[1];
     const int64_t slot = token_slot[u];
     if (side != 0 && slot < 0) continue;
-    const __half* row = a.src[side] + i * a.ld[side];
-    const int e0 = g * G + lane * E;
-    const V raw = *reinterpret_cast<const V*>(row + e0);
-    const __half* h = reinterpret_cast<const __half*>(&raw);
-    float x[E];
-#pragma unroll
-    for (int j = 0; j < E; ++j) x[j] = __half2float(h[j]);
+    g = g * per + lg;                                       // this lane's group
+    const bool mine = g < (side == 0 ? a.jobs[0] : side == 1 ? a.jobs[1] : a.jobs[2]);
+    const __half* row = (side == 0 ? a.src[0] + i * a.ld[0] : side == 1 ? a.src[1] + i * a.ld[1]
+                                                                         : a.src[2] + i * a.ld[2]) +
+                        (mine ? g * v.group : 0);
+    float x[kLane];
+    load_16(row + in_group, x);
     if (side != 2) {
-      if (a.inv_freq != nullptr) {
-        const int d = v.head_dim, h0 = e0 & (d - 1);
-        float o[E];                                         // the partners
+      const int h0 = in_group & (v.head_dim - 1);
+      if (a.inv_freq != nullptr && h0 < 2 * a.pairs) {
         if (a.interleaved) {
 #pragma unroll
-          for (int j = 0; j < E; ++j) o[j] = x[j ^ 1];
-        } else if (a.pairs % E == 0) {                      // a lane's elements share one side
-          V rawp = raw;
-          if (h0 < 2 * a.pairs)
-            rawp = *reinterpret_cast<const V*>(row + (h0 < a.pairs ? e0 + a.pairs : e0 - a.pairs));
-          const __half* hp = reinterpret_cast<const __half*>(&rawp);
+          for (int j = 0; j < kLane; j += 2) {
+            const int p = (h0 + j) >> 1;
+            if (p < a.pairs) {
+              const float c = turn[u][0][p], s = turn[u][1][p], xa = x[j], xb = x[j + 1];
+              x[j] = __fsub_rn(__fmul_rn(xa, c), __fmul_rn(xb, s));
+              x[j + 1] = __fadd_rn(__fmul_rn(xb, c), __fmul_rn(xa, s));
+            }
+          }
+        } else if (a.pairs % kLane == 0) {                  // a lane's elements share one side
+          const bool second = h0 >= a.pairs;
+          float o[kLane];                                   // the partners
+          load_16(row + in_group + (second ? -a.pairs : a.pairs), o);
+          const float4* c = reinterpret_cast<const float4*>(turn[u][0] + (second ? h0 - a.pairs : h0));
+          const float4* s = reinterpret_cast<const float4*>(turn[u][second ? 1 : 2] + (second ? h0 - a.pairs : h0));
 #pragma unroll
-          for (int j = 0; j < E; ++j) o[j] = __half2float(hp[j]);
+          for (int j = 0; j < kLane; j += 4) {
+            const float4 cj = c[j / 4], sj = s[j / 4];
+            f2_unpack(f2_add(f2_mul(f2_pack(x[j], x[j + 1]), f2_pack(cj.x, cj.y)),
+                             f2_mul(f2_pack(o[j], o[j + 1]), f2_pack(sj.x, sj.y))), x[j], x[j + 1]);
+            f2_unpack(f2_add(f2_mul(f2_pack(x[j + 2], x[j + 3]), f2_pack(cj.z, cj.w)),
+                             f2_mul(f2_pack(o[j + 2], o[j + 3]), f2_pack(sj.z, sj.w))), x[j + 2], x[j + 3]);
+          }
         } else {
 #pragma unroll
-          for (int j = 0; j < E; ++j) {
-            const int hh = h0 + j;
-            o[j] = hh < 2 * a.pairs
-                       ? __half2float(row[hh < a.pairs ? e0 + j + a.pairs : e0 + j - a.pairs])
-                       : 0.0f;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          int partner;
-          bool second;
-          const int p = rope_pair(a, h0 + j, &partner, &second);
-          if (p >= 0) {
-            const float2 cs = turn[u][p];
-            const float xc = __fmul_rn(x[j], cs.x), os = __fmul_rn(o[j], cs.y);
-            x[j] = second ? __fadd_rn(xc, os) : __fsub_rn(xc, os);
+          for (int j = 0; j < kLane; ++j) {
+            const int h = h0 + j;
+            if (h < 2 * a.pairs) {
+              const bool second = h >= a.pairs;
+              const int p = second ? h - a.pairs : h;
+              const float o = __half2float(row[in_group + j + (second ? -a.pairs : a.pairs)]);
+              x[j] = __fadd_rn(__fmul_rn(x[j], turn[u][0][p]), __fmul_rn(o, turn[u][second ? 1 : 2][p]));
+            }
           }
         }
       }
+      wht_stages<0, 4>(x);                                  // the element bits held by the lane
 #pragma unroll
-      for (int b = 0; b < LE; ++b)
+      for (int lb = 0; lb < 4; ++lb)
+        if (4 + lb < a.head_bits) {                         // bits of the lane: x + o, or o - x
+          const float sign = (lane >> lb) & 1 ? -1.0f : 1.0f;
+          const uint64_t sign2 = f2_pack(sign, sign);
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-          if (!(j & (1 << b))) {
-            const float p = x[j], q = x[j | (1 << b)];
-            x[j] = p + q;
-            x[j | (1 << b)] = p - q;
-          }
-#pragma unroll
-      for (int lb = 0; lb < 5; ++lb)
-        if (LE + lb < a.head_bits) {
-          const bool upper = (lane >> lb) & 1;
-#pragma unroll
-          for (int j = 0; j < E; ++j) {
-            const float o = __shfl_xor_sync(0xffffffffu, x[j], 1 << lb);
-            x[j] = upper ? o - x[j] : x[j] + o;
+          for (int j = 0; j < kLane; j += 2) {
+            const float o0 = __shfl_xor_sync(0xffffffffu, x[j], 1 << lb), o1 = __shfl_xor_sync(0xffffffffu, x[j + 1], 1 << lb);
+            f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), sign2, f2_pack(o0, o1)), x[j], x[j + 1]);
           }
         }
     }
     if (side == 0) {
-      V out;
-      __half* oh = reinterpret_cast<__half*>(&out);
+      if (!mine) continue;
+      const uint64_t unit = f2_pack(a.inv_sqrt, a.inv_sqrt);
+      __half2 out[8];
 #pragma unroll
-      for (int j = 0; j < E; ++j) oh[j] = __float2half_rn(x[j] * a.inv_sqrt);
-      *reinterpret_cast<V*>(a.q_rot + static_cast<int64_t>(i) * a.q_width + e0) = out;
+      for (int j = 0; j < kLane; j += 2) {
+        float y0, y1;
+        f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), unit), y0, y1);
+        out[j / 2] = __floats2half2_rn(y0, y1);
+      }
+      uint4* to = reinterpret_cast<uint4*>(a.q_rot + static_cast<int64_t>(i) * a.q_width + g * v.group + in_group);
+      to[0] = reinterpret_cast<const uint4*>(out)[0];
+      to[1] = reinterpret_cast<const uint4*>(out)[1];
       continue;
     }
     float mx = x[0], mn = x[0];
 #pragma unroll
-    for (int j = 1; j < E; ++j) {
+    for (int j = 1; j < kLane; ++j) {
       mx = fmaxf(mx, x[j]);
       mn = fminf(mn, x[j]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
     }
+    if (!mine) continue;
     const int64_t at = slot * v.groups + g;
-    const RowQ q = asym_row_q(mn, mx, 1.0f, side == 1 ? a.inv_sqrt : 1.0f,
-                              lane == 0 ? v.scales[side - 1] + at : nullptr,
-                              v.zeros[side - 1] + at);
-    C packed = 0;
+    float* scale = (side == 1 ? v.scales[0] : v.scales[1]) + at;
+    int32_t* zero = (side == 1 ? v.zeros[0] : v.zeros[1]) + at;
+    const RowQ q = asym_row_q(mn, mx, 1.0f, side == 1 ? a.inv_sqrt : 1.0f, in_group == 0 ? scale : nullptr, zero);
+    float lo8[8], hi8[8];
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float t = fminf(fmaxf(fmaf(x[j], q.r, q.c), q.lo), q.hi);
-      packed |= static_cast<C>((__float_as_uint(t) & 0xFu) << (4 * j));
+    for (int j = 0; j < 8; ++j) {
+      lo8[j] = x[j];
+      hi8[j] = x[8 + j];
     }
-    *reinterpret_cast<C*>(v.codes[side - 1] + at * (G / 2) + lane * (E / 2)) = packed;
+    *reinterpret_cast<uint2*>((side == 1 ? v.codes[0] : v.codes[1]) + at * (v.group / 2) + in_group / 2) =
+        make_uint2(quant_word<true>(lo8, q.r, q.c, q.lo, q.hi), quant_word<true>(hi8, q.r, q.c, q.lo, q.hi));
   }
 }
 
-// One warp per group of a token's row: E codes a lane, one fp16 vector store.
-template <int E>
-__global__ void __launch_bounds__(256) kv_dequantize_kernel(KvView v, __half* k_out,
-                                                            __half* v_out) {
+// A warp takes 512 values of a token's row at a time, 16 a lane: 8 bytes of codes in, two 16-byte stores out.
+__global__ void __launch_bounds__(256) kv_dequantize_kernel(KvView v, __half* k_out, __half* v_out) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int G = 32 * E;
-  using V = typename std::conditional<E == 4, uint2, uint4>::type;
-  using C = typename std::conditional<E == 4, uint16_t, uint32_t>::type;
   const int lane = threadIdx.x & 31;
   const int32_t i = blockIdx.x;
   const int32_t b = kv_seq_of_row(v, i);
@@ -237,27 +237,42 @@ __global__ void __launch_bounds__(256) kv_dequantize_kernel(KvView v, __half* k_
   if (i < c0 || c0 < 0) return;
   const int32_t t = kv_len(v, b) - (c1 - i);
   const int64_t slot = t >= 0 ? kv_slot(v, v.table, b, t) : -1;
-  const int first = k_out != nullptr ? 0 : v.groups, last = v_out != nullptr ? 2 * v.groups : v.groups;
+  const int jobs = (v.width + 511) / 512;
+  const int first = k_out != nullptr ? 0 : jobs, last = v_out != nullptr ? 2 * jobs : jobs;
   for (int job = first + (threadIdx.x >> 5); job < last; job += 8) {
-    const int side = job >= v.groups;
-    const int g = job - side * v.groups;
-    V out;
-    __half* oh = reinterpret_cast<__half*>(&out);
+    const bool values = job >= jobs;
+    const int e0 = (values ? job - jobs : job) * 512 + lane * kLane;
+    if (e0 >= v.width) continue;
+    __half2 out[8];
 #pragma unroll
-    for (int j = 0; j < E; ++j) oh[j] = __float2half_rn(0.0f);
+    for (int j = 0; j < 8; ++j) out[j] = __floats2half2_rn(0.0f, 0.0f);
     if (slot >= 0) {
-      const int64_t at = slot * v.groups + g;
-      const float s = v.scales[side][at];
-      const int32_t z = v.zeros[side][at];
-      const C c = *reinterpret_cast<const C*>(v.codes[side] + at * (G / 2) + lane * (E / 2));
+      const int64_t at = slot * v.groups + e0 / v.group;
+      const float s = (values ? v.scales[1] : v.scales[0])[at];
+      const int32_t z = (values ? v.zeros[1] : v.zeros[0])[at];
+      const uint2 w = *reinterpret_cast<const uint2*>((values ? v.codes[1] : v.codes[0]) + slot * (v.width / 2) + e0 / 2);
+      if (z > -4000000 && z < 4000000) {
+        // u = c + 8 in the low bits of 2^23: 2^23 + u - (2^23 + 8 + z) is c - z, exact
+        const float off = 8388616.0f + static_cast<float>(z);
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int32_t code = static_cast<int32_t>(((c >> (4 * j)) & 0xF) ^ 8) - 8;
-        oh[j] = __float2half_rn(s * static_cast<float>(static_cast<int64_t>(code) - z));
+        for (int j = 0; j < kLane; j += 2) {
+          const uint32_t x = ((j < 8 ? w.x : w.y) >> (4 * (j & 7))) ^ 0x88u;
+          const float y0 = __uint_as_float((x & 15u) | 0x4B000000u) - off;
+          const float y1 = __uint_as_float(((x >> 4) & 15u) | 0x4B000000u) - off;
+          out[j / 2] = __floats2half2_rn(s * y0, s * y1);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kLane; j += 2) {
+          const uint32_t x = ((j < 8 ? w.x : w.y) >> (4 * (j & 7))) ^ 0x88u;
+          const int64_t c1 = static_cast<int64_t>(x & 15u) - 8, c2 = static_cast<int64_t>((x >> 4) & 15u) - 8;
+          out[j / 2] = __floats2half2_rn(s * static_cast<float>(c1 - z), s * static_cast<float>(c2 - z));
+        }
       }
     }
-    __half* dst = side == 0 ? k_out : v_out;
-    *reinterpret_cast<V*>(dst + static_cast<int64_t>(i) * v.width + g * G + lane * E) = out;
+    uint4* to = reinterpret_cast<uint4*>((values ? v_out : k_out) + static_cast<int64_t>(i) * v.width + e0);
+    to[0] = reinterpret_cast<const uint4*>(out)[0];
+    to[1] = reinterpret_cast<const uint4*>(out)[1];
   }
 }
 
@@ -291,12 +306,13 @@ qr_status launch_kv_append(const KvView& v, const KvAppendJob& j, cudaStream_t s
   const int jobs = a.jobs[0] + a.jobs[1] + a.jobs[2];
   if (jobs == 0) return QR_OK;
   const unsigned blocks = (v.tokens + kTokensPerBlock - 1) / kTokensPerBlock;
-  // few tokens: several blocks share the groups of theirs, up to one group a warp
-  const int most = (kTokensPerBlock * jobs + kAppendWarps - 1) / kAppendWarps;
+  // few tokens: several blocks share the groups of theirs, up to one job a warp
+  const int per = 32 * kLane / v.group;
+  const int warps = kTokensPerBlock * ((a.jobs[0] + per - 1) / per + (a.jobs[1] + per - 1) / per + (a.jobs[2] + per - 1) / per);
+  const int most = (warps + kAppendWarps - 1) / kAppendWarps;
   const unsigned split = std::max(1, std::min<int>(most, 4 * sm_count() / static_cast<int>(std::min(blocks, 1u << 20))));
   const dim3 grid(blocks, split), block(32 * kAppendWarps);
-  cudaError_t e = v.group == 128 ? launch_pdl(kv_append_kernel<4>, grid, block, 0, stream, 1, a)
-                                 : launch_pdl(kv_append_kernel<8>, grid, block, 0, stream, 1, a);
+  cudaError_t e = launch_pdl(kv_append_kernel, grid, block, 0, stream, 1, a);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? QR_OK : QR_ERR_CUDA;
 }
@@ -306,9 +322,7 @@ qr_status launch_kv_dequantize(const KvView& v, uint16_t* k_out, uint16_t* v_out
   const dim3 grid(v.tokens), block(256);
   auto* k = reinterpret_cast<__half*>(k_out);
   auto* w = reinterpret_cast<__half*>(v_out);
-  cudaError_t e = v.group == 128
-                      ? launch_pdl(kv_dequantize_kernel<4>, grid, block, 0, stream, 1, v, k, w)
-                      : launch_pdl(kv_dequantize_kernel<8>, grid, block, 0, stream, 1, v, k, w);
+  cudaError_t e = launch_pdl(kv_dequantize_kernel, grid, block, 0, stream, 1, v, k, w);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? QR_OK : QR_ERR_CUDA;
 }
