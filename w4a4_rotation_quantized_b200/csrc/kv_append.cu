@@ -9,8 +9,8 @@
 //
 // 2 (H_q + 2 H_k) d bytes read and 2 H_q d + H_k (d + 16 d / g) written a token, against some 14 operations an
 // element: a lane holds 16 consecutive elements, so that four of the butterfly's stages run in registers (on
-// pairs of fp32) and only those above them by shuffles (4 elements a lane: 276 us for 6200 tokens of 32 + 2 x 32
-// heads; the issue of 250 instructions for 128 elements bound it).  A rope turns (i, i + pairs): the lane reads
+// pairs of fp32) and only those above them by shuffles (103 us for 6200 tokens of 32 + 2 x 32 heads of 128, 276
+// with 4 elements a lane: the issue of 250 instructions for 128 elements bound it).  A rope turns (i, i + pairs): the lane reads
 // its elements' partners from memory a second time (they are in L1, since another lane just asked for them), which
 // is cheaper to address than shuffles whose distance depends on the number of pairs.  The angles depend on the
 // token alone, not on the head: a block forms the sines and cosines of its tokens once, in double precision
@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kAppendWarps = 8;
 constexpr int kMaxPairs = 128;             // head_dim / 2
-constexpr int kTokensPerBlock = 4;
+constexpr int kTokensPerBlock = 4;         // at most; one where tokens are few
 
 struct AppendArgs {
   KvView v;
@@ -43,8 +43,8 @@ struct AppendArgs {
   const int32_t* positions;
   int64_t ld_pos;
   int32_t pairs, axes, interleaved;
-  int32_t head_bits;
   float inv_sqrt;
+  int32_t per_block;                       // tokens of a block
 };
 
 constexpr int kLane = 16;                 // elements of a lane
@@ -63,18 +63,24 @@ __device__ __forceinline__ void load_16(const __half* p, float (&x)[kLane]) {
   }
 }
 
-__global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const AppendArgs a) {
+// Place of pair p in a table of cosines or sines: 16 pairs (a lane's) 80 bytes apart, so that eight lanes' 16-byte
+// reads meet all banks.
+__device__ __forceinline__ int pair_at(int p) { return p + (p >> 4) * 4; }
+
+// D: head_dim; G: group.
+template <int D, int G>
+__global__ void __launch_bounds__(32 * kAppendWarps, 4) kv_append_kernel(const AppendArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   // of the block's tokens: cosines, sines and sines with the other sign
-  __shared__ __align__(16) float turn[kTokensPerBlock][3][kMaxPairs];
+  __shared__ __align__(16) float turn[kTokensPerBlock][3][kMaxPairs / 16 * 20];
   __shared__ int32_t token_seq[kTokensPerBlock];
   __shared__ int64_t token_slot[kTokensPerBlock];           // -1: no place for k and v
   const KvView& v = a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t i0 = blockIdx.x * kTokensPerBlock;
+  const int32_t i0 = blockIdx.x * a.per_block;
 
-  if (warp < kTokensPerBlock) {
+  if (warp < a.per_block) {
     const int32_t i = i0 + warp;
     int32_t b = v.batch;
     int64_t slot = -1;
@@ -95,7 +101,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
     }
   }
   if (a.inv_freq != nullptr) {
-    for (int p = threadIdx.x; p < kTokensPerBlock * a.pairs; p += blockDim.x) {
+    for (int p = threadIdx.x; p < a.per_block * a.pairs; p += blockDim.x) {
       const int u = p / a.pairs, j = p - u * a.pairs;
       if (i0 + u >= v.tokens) break;
       const int32_t ax = a.axis != nullptr ? a.axis[j] : 0;
@@ -103,43 +109,42 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
       if (ax >= 0 && ax < a.axes)
         sincos(static_cast<double>(a.positions[ax * a.ld_pos + i0 + u]) *
                    static_cast<double>(a.inv_freq[j]), &s, &c);
-      turn[u][0][j] = static_cast<float>(c);
-      turn[u][1][j] = static_cast<float>(s);
-      turn[u][2][j] = -static_cast<float>(s);
+      turn[u][0][pair_at(j)] = static_cast<float>(c);
+      turn[u][1][pair_at(j)] = static_cast<float>(s);
+      turn[u][2][pair_at(j)] = -static_cast<float>(s);
     }
   }
   __syncthreads();
 
-  const int lanes = v.group / kLane, per = 32 / lanes;      // lanes of a group, groups of a warp
+  constexpr int lanes = G / kLane, per = 32 / lanes;        // lanes of a group, groups of a warp
   const int lg = lane / lanes, in_group = lane % lanes * kLane;
-  const int jobs_of[3] = {(a.jobs[0] + per - 1) / per, (a.jobs[1] + per - 1) / per, (a.jobs[2] + per - 1) / per};
-  const int per_token = jobs_of[0] + jobs_of[1] + jobs_of[2];
-  const int jobs = kTokensPerBlock * per_token;
-  for (int job = blockIdx.y * kAppendWarps + warp; job < jobs; job += gridDim.y * kAppendWarps) {
-    const int u = job / per_token;
-    int g = job - u * per_token;
+  const int jq = (a.jobs[0] + per - 1) / per, jk = jq + (a.jobs[1] + per - 1) / per;
+  const int per_token = jk + (a.jobs[2] + per - 1) / per;
+#pragma unroll 1
+  for (int u = 0; u < a.per_block; ++u)
+#pragma unroll 1
+    for (int job = blockIdx.y * kAppendWarps + warp; job < per_token; job += gridDim.y * kAppendWarps) {
     const int32_t i = i0 + u;
-    if (i >= v.tokens || token_seq[u] >= v.batch) continue;      // uniform over the warp
-    const int side = g < jobs_of[0] ? 0 : g < jobs_of[0] + jobs_of[1] ? 1 : 2;
-    g -= side == 0 ? 0 : side == 1 ? jobs_of[0] : jobs_of[0] + jobs_of[1];
+    if (i >= v.tokens || token_seq[u] >= v.batch) break;         // uniform over the warp
+    const int side = job < jq ? 0 : job < jk ? 1 : 2;
     const int64_t slot = token_slot[u];
-    if (side != 0 && slot < 0) continue;
-    g = g * per + lg;                                       // this lane's group
+    if (side != 0 && slot < 0) break;
+    const int g = (job - (side == 0 ? 0 : side == 1 ? jq : jk)) * per + lg;      // this lane's group
     const bool mine = g < (side == 0 ? a.jobs[0] : side == 1 ? a.jobs[1] : a.jobs[2]);
     const __half* row = (side == 0 ? a.src[0] + i * a.ld[0] : side == 1 ? a.src[1] + i * a.ld[1]
                                                                          : a.src[2] + i * a.ld[2]) +
-                        (mine ? g * v.group : 0);
+                        (mine ? g * G : 0);
     float x[kLane];
     load_16(row + in_group, x);
     if (side != 2) {
-      const int h0 = in_group & (v.head_dim - 1);
+      const int h0 = in_group & (D - 1);
       if (a.inv_freq != nullptr && h0 < 2 * a.pairs) {
         if (a.interleaved) {
 #pragma unroll
           for (int j = 0; j < kLane; j += 2) {
             const int p = (h0 + j) >> 1;
             if (p < a.pairs) {
-              const float c = turn[u][0][p], s = turn[u][1][p], xa = x[j], xb = x[j + 1];
+              const float c = turn[u][0][pair_at(p)], s = turn[u][1][pair_at(p)], xa = x[j], xb = x[j + 1];
               x[j] = __fsub_rn(__fmul_rn(xa, c), __fmul_rn(xb, s));
               x[j + 1] = __fadd_rn(__fmul_rn(xb, c), __fmul_rn(xa, s));
             }
@@ -148,8 +153,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
           const bool second = h0 >= a.pairs;
           float o[kLane];                                   // the partners
           load_16(row + in_group + (second ? -a.pairs : a.pairs), o);
-          const float4* c = reinterpret_cast<const float4*>(turn[u][0] + (second ? h0 - a.pairs : h0));
-          const float4* s = reinterpret_cast<const float4*>(turn[u][second ? 1 : 2] + (second ? h0 - a.pairs : h0));
+          const float4* c = reinterpret_cast<const float4*>(turn[u][0] + pair_at(second ? h0 - a.pairs : h0));
+          const float4* s = reinterpret_cast<const float4*>(turn[u][second ? 1 : 2] + pair_at(second ? h0 - a.pairs : h0));
 #pragma unroll
           for (int j = 0; j < kLane; j += 4) {
             const float4 cj = c[j / 4], sj = s[j / 4];
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
               const bool second = h >= a.pairs;
               const int p = second ? h - a.pairs : h;
               const float o = __half2float(row[in_group + j + (second ? -a.pairs : a.pairs)]);
-              x[j] = __fadd_rn(__fmul_rn(x[j], turn[u][0][p]), __fmul_rn(o, turn[u][second ? 1 : 2][p]));
+              x[j] = __fadd_rn(__fmul_rn(x[j], turn[u][0][pair_at(p)]), __fmul_rn(o, turn[u][second ? 1 : 2][pair_at(p)]));
             }
           }
         }
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
       wht_stages<0, 4>(x);                                  // the element bits held by the lane
 #pragma unroll
       for (int lb = 0; lb < 4; ++lb)
-        if (4 + lb < a.head_bits) {                         // bits of the lane: x + o, or o - x
+        if ((16 << lb) < D) {                               // bits of the lane: x + o, or o - x
           const float sign = (lane >> lb) & 1 ? -1.0f : 1.0f;
           const uint64_t sign2 = f2_pack(sign, sign);
 #pragma unroll
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
         f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), unit), y0, y1);
         out[j / 2] = __floats2half2_rn(y0, y1);
       }
-      uint4* to = reinterpret_cast<uint4*>(a.q_rot + static_cast<int64_t>(i) * a.q_width + g * v.group + in_group);
+      uint4* to = reinterpret_cast<uint4*>(a.q_rot + static_cast<int64_t>(i) * a.q_width + g * G + in_group);
       to[0] = reinterpret_cast<const uint4*>(out)[0];
       to[1] = reinterpret_cast<const uint4*>(out)[1];
       continue;
@@ -205,6 +210,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
       mx = fmaxf(mx, x[j]);
       mn = fminf(mn, x[j]);
     }
+#pragma unroll
     for (int o = lanes >> 1; o > 0; o >>= 1) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -220,7 +226,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
       lo8[j] = x[j];
       hi8[j] = x[8 + j];
     }
-    *reinterpret_cast<uint2*>((side == 1 ? v.codes[0] : v.codes[1]) + at * (v.group / 2) + in_group / 2) =
+    *reinterpret_cast<uint2*>((side == 1 ? v.codes[0] : v.codes[1]) + at * (G / 2) + in_group / 2) =
         make_uint2(quant_word<true>(lo8, q.r, q.c, q.lo, q.hi), quant_word<true>(hi8, q.r, q.c, q.lo, q.hi));
   }
 }
@@ -301,18 +307,27 @@ qr_status launch_kv_append(const KvView& v, const KvAppendJob& j, cudaStream_t s
     a.axes = j.rope->axes;
     a.interleaved = j.rope->interleaved;
   }
-  while ((1 << a.head_bits) < v.head_dim) ++a.head_bits;
   a.inv_sqrt = static_cast<float>(1.0 / std::sqrt(static_cast<double>(v.head_dim)));
   const int jobs = a.jobs[0] + a.jobs[1] + a.jobs[2];
   if (jobs == 0) return QR_OK;
-  const unsigned blocks = (v.tokens + kTokensPerBlock - 1) / kTokensPerBlock;
+  a.per_block = v.tokens <= 4 * sm_count() ? 1 : kTokensPerBlock;
+  const unsigned blocks = (v.tokens + a.per_block - 1) / a.per_block;
   // few tokens: several blocks share the groups of theirs, up to one job a warp
   const int per = 32 * kLane / v.group;
-  const int warps = kTokensPerBlock * ((a.jobs[0] + per - 1) / per + (a.jobs[1] + per - 1) / per + (a.jobs[2] + per - 1) / per);
+  const int warps = (a.jobs[0] + per - 1) / per + (a.jobs[1] + per - 1) / per + (a.jobs[2] + per - 1) / per;
   const int most = (warps + kAppendWarps - 1) / kAppendWarps;
   const unsigned split = std::max(1, std::min<int>(most, 4 * sm_count() / static_cast<int>(std::min(blocks, 1u << 20))));
   const dim3 grid(blocks, split), block(32 * kAppendWarps);
-  cudaError_t e = launch_pdl(kv_append_kernel, grid, block, 0, stream, 1, a);
+  auto run = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, stream, 1, a); };
+  cudaError_t e;
+  if (v.group == 128)
+    e = v.head_dim == 32 ? run(kv_append_kernel<32, 128>) : v.head_dim == 64 ? run(kv_append_kernel<64, 128>)
+                                                          : run(kv_append_kernel<128, 128>);
+  else
+    e = v.head_dim == 32    ? run(kv_append_kernel<32, 256>)
+        : v.head_dim == 64  ? run(kv_append_kernel<64, 256>)
+        : v.head_dim == 128 ? run(kv_append_kernel<128, 256>)
+                            : run(kv_append_kernel<256, 256>);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? QR_OK : QR_ERR_CUDA;
 }
