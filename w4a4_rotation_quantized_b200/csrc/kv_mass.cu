@@ -11,8 +11,9 @@
 // one group and 32 tokens at a time, kSteps times, the next ones under way in a ring in shared memory; warps of
 // a block take neighbouring groups of the same tokens.
 // Many rows: a warp keeps 32 tokens' keys as operands in registers (16 where a head is 256 wide) and the block's
-// eight warps go through the query rows together, 32 at a time through shared memory: bound by the issue of the
-// products and of the exponentials, about 25 instructions for 8 rows, 32 tokens and lane.
+// eight warps go through the query rows together, 64 at a time through shared memory.  Under a causal mask the first
+// tokens meet the most rows, so four blocks, a cluster, share the rows of 256 tokens and the first adds their sums up
+// in order (a prompt of 2048 tokens, 32 heads: 247 us with one block of 8 warps an SM and all rows, 120 so).
 #include <algorithm>
 #include <cmath>
 
@@ -27,7 +28,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSteps = 4;                      // of 32 tokens, of a warp (few rows)
-constexpr int kRowsStaged = 32;                // query rows in shared memory (many rows)
+constexpr int kRowsStaged = 64;                // query rows in shared memory (many rows)
+constexpr int kShare = 4;                      // blocks that share the rows (many rows)
 
 struct MassArgs {
   KvView v;
@@ -258,12 +260,18 @@ struct Many {
   static constexpr int kTiles = D == 256 ? 1 : 2;              // of 16 tokens, of a warp
   static constexpr int kTokens = 16 * kTiles;
   static constexpr int kFrag = kRowsStaged / 8 * (D / 32) * 32;        // 16-byte entries of the staged queries
-  static constexpr int kBytes = 2 * kFrag * 16 + 2 * kRowsStaged * 16;
+  static constexpr int kBytes = 2 * kFrag * 16 + 2 * kRowsStaged * 16 + kWarps * kTokens * 4;
 };
 
-// Many rows.  grid: (blocks of 8 kTokens tokens, groups, sequences)
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+
+// Many rows.  grid: (kShare times blocks of 8 kTokens tokens, groups, sequences), clusters of kShare
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_mass_many_kernel(const MassArgs a) {
+__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_mass_many_kernel(const MassArgs a) {
   using M = Many<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   const KvView& v = a.v;
@@ -276,12 +284,14 @@ __global__ void __launch_bounds__(kThreads) kv_mass_many_kernel(const MassArgs a
   const SeqRows rows = seq_rows(v, b);
   const int32_t all_rows = rows.here * a.gq;
   const int32_t n_seen = all_rows > 0 ? seen(rows, rows.here - 1, a.causal) : 0;
-  const int32_t block0 = blockIdx.x * (kWarps * M::kTokens);
-  if (block0 >= n_seen) return;                          // (the whole block)
+  const int32_t block0 = blockIdx.x / kShare * (kWarps * M::kTokens);
+  const int share = blockIdx.x % kShare;
+  if (block0 >= n_seen) return;                          // (the whole cluster)
   const int32_t t0 = block0 + warp * M::kTokens;
-  // the first new token that sees the block's first token, and the first that sees its last
+  // this block's share of the rows, from the first new token that sees the block's first token on
   const int32_t first_row = a.causal ? max(block0 - rows.before, 0) * a.gq : 0;
-  const int row0 = first_row / kRowsStaged * kRowsStaged;
+  const int row0 = (first_row / kRowsStaged + share) * kRowsStaged;
+  constexpr int kStride = kShare * kRowsStaged;
 
   int32_t slot[M::kTiles][2];                            // of tokens g and g + 8 of each tile
 #pragma unroll
@@ -356,9 +366,9 @@ __global__ void __launch_bounds__(kThreads) kv_mass_many_kernel(const MassArgs a
     __syncthreads();
     stage(row0, 0);
     int buf = 0;
-    for (int32_t r0 = row0; r0 < all_rows; r0 += kRowsStaged, buf ^= 1) {
+    for (int32_t r0 = row0; r0 < all_rows; r0 += kStride, buf ^= 1) {
       __syncthreads();
-      if (r0 + kRowsStaged < all_rows) stage(r0 + kRowsStaged, buf ^ 1);
+      if (r0 + kStride < all_rows) stage(r0 + kStride, buf ^ 1);
 #pragma unroll 1
       for (int e = 0; e < kRowsStaged / 8; ++e) {
         if (r0 + 8 * e >= all_rows) break;
@@ -381,6 +391,8 @@ __global__ void __launch_bounds__(kThreads) kv_mass_many_kernel(const MassArgs a
       }
     }
   }
+  // the cluster's sums, added up by its first block
+  float* own = reinterpret_cast<float*>(smem + 2 * M::kFrag * 16 + 2 * kRowsStaged * 16) + warp * M::kTokens;
 #pragma unroll
   for (int h = 0; h < M::kTiles; ++h)
 #pragma unroll
@@ -388,9 +400,17 @@ __global__ void __launch_bounds__(kThreads) kv_mass_many_kernel(const MassArgs a
       float x = sum[h][e];
       x += __shfl_xor_sync(0xffffffffu, x, 1);
       x += __shfl_xor_sync(0xffffffffu, x, 2);
-      if (c == 0 && slot[h][e] >= 0)
-        a.mass[(static_cast<int64_t>(b) * v.groups + j) * a.ld_mass + t0 + 16 * h + 8 * e + g] += x;
+      if (c == 0) own[16 * h + 8 * e + g] = x;
     }
+  cluster_sync();
+  if (share == 0 && lane < M::kTokens) {
+    const int32_t t = t0 + lane;
+    float x = own[lane];
+    for (int k = 1; k < kShare; ++k) x += ld_cluster_f32(mapa_shared(smem_u32(own + lane), k));
+    if (t < n_seen && kv_slot(v, v.table, b, t) >= 0)
+      a.mass[(static_cast<int64_t>(b) * v.groups + j) * a.ld_mass + t] += x;
+  }
+  cluster_sync();
 }
 
 // Rows of a sequence and key head (on average) up to which keys are streamed.
@@ -405,8 +425,8 @@ cudaError_t run_mass(MassArgs& a, cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(kv_mass_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Many<D>::kBytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv_mass_many_kernel<D>, dim3((v.capacity + block - 1) / block, v.groups, v.batch),
-                      dim3(kThreads), Many<D>::kBytes, stream, 1, a);
+    return launch_pdl(kv_mass_many_kernel<D>, dim3(kShare * ((v.capacity + block - 1) / block), v.groups, v.batch),
+                      dim3(kThreads), Many<D>::kBytes, stream, kShare, a);
   }
   while (a.groups_log2 < 3 && v.groups % (2 << a.groups_log2) == 0) ++a.groups_log2;
   const int block = 32 * kSteps * (kWarps >> a.groups_log2);
