@@ -417,7 +417,8 @@ QR_API qr_status qr_kv_quantize(const uint16_t* Q, const uint16_t* K, const uint
  * qr_kv_quantize writes: codes uint8 [slots x W/2] (W = heads * head_dim,
  * element 2j in the low nibble, two's complement), scales float32 and zeros int32
  * [slots x W/group]; a value is scale * (code - zero).  Keys stand in the basis of
- * R3.  head_dim in {32, 64, 128, 256}; group 128 or 256, a multiple of head_dim
+ * R3.  Scales are not negative; in attention a value scale below 2^-40 counts as 0, and
+ * one above 2^40 need not give finite outputs.  head_dim in {32, 64, 128, 256}; group 128 or 256, a multiple of head_dim
  * that divides W; W <= 65536; codes 16-byte aligned, scales and zeros 4-byte.
  * The rows are pages of page_size slots; a tail of slots that fills no page
  * is never used.
@@ -435,7 +436,7 @@ QR_API qr_status qr_kv_quantize(const uint16_t* Q, const uint16_t* K, const uint
  * the arrays are not touched.  Pages may be shared between sequences for reading;
  * a page that two sequences (or two places of one) write in one call is
  * left with some mixture of the two.
- * batch <= 4096, max_pages * page_size < 2^30. */
+ * batch <= 4096, max_pages * page_size < 2^30, slots < 2^31. */
 typedef struct {
   uint8_t* k_codes;
   float* k_scales;

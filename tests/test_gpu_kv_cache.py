@@ -155,6 +155,25 @@ def test_append_parts_places_and_rows_of_nobody():
     assert torch.equal(Q.kv_append(seqs, q, None, None)[1:16], out[1:16])
 
 
+def test_offsets_that_do_not_ascend_are_not_followed():
+    """Row offsets of a broken batch: nothing outside the sequences' tokens is read or written."""
+    rng = np.random.default_rng(6)
+    hk, d, page = 2, 128, 16
+    x = [dev(rng.standard_normal((8, h * d)).astype(np.float16)) for h in (4, hk, hk)]
+    for cu in ([0, 7, 2, 4], [3, 3, -5, 8], [0, 100, 2, 9], [-4, 2, 5, 8]):
+        cache = Q.KVCache.empty(3, page, hk, d)
+        seqs = sequences(cache, [9, 16, 3], cu, None)
+        q = Q.kv_append(seqs, *x)
+        Q.kv_dequantize(seqs, 8)
+        q = torch.where(torch.isfinite(q), q, torch.zeros_like(q))        # rows of nobody are not written
+        out, lse = Q.kv_attention(seqs, q, return_lse=True)
+        lse = torch.where(torch.isfinite(lse), lse, torch.full_like(lse, 50.0))
+        Q.kv_attention_mass(seqs, q, lse, torch.zeros((3, hk, page), device="cuda"))
+        torch.cuda.synchronize()
+        written = np.nonzero(host(cache.keys[1]).any(1))[0]
+        assert all(r % page < n for r, n in zip(written, np.array([9, 16, 3])[written // page]))
+
+
 EVICTS = [
     # heads, head_dim, group, page, lens, keep, recent
     (2, 128, 128, 16, [100, 40, 0, 64], 40, 8),

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 4) kv_append_kernel(const A
       b = kv_seq_of_row(v, i);
       if (b < v.batch) {
         const int32_t c0 = v.cu[b], c1 = v.cu[b + 1];
-        if (i < c0 || c0 < 0) b = v.batch;                  // offsets that do not ascend
+        if (i < c0 || i >= c1 || c0 < 0) b = v.batch;       // offsets that do not ascend
         else {
           const int32_t t = kv_len(v, b) - (c1 - i);
           if (t >= 0) slot = kv_slot(v, v.table, b, t);
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(256) kv_dequantize_kernel(KvView v, __half* k_
   const int32_t b = kv_seq_of_row(v, i);
   if (b >= v.batch) return;
   const int32_t c0 = v.cu[b], c1 = v.cu[b + 1];
-  if (i < c0 || c0 < 0) return;
+  if (i < c0 || i >= c1 || c0 < 0) return;
   const int32_t t = kv_len(v, b) - (c1 - i);
   const int64_t slot = t >= 0 ? kv_slot(v, v.table, b, t) : -1;
   const int jobs = (v.width + 511) / 512;

@@ -586,8 +586,9 @@ cudaError_t run_join(const SplitArgs& a, bool prefill, cudaStream_t stream) {
 template <int D, int NC>
 cudaError_t run_split(const SplitArgs& a, cudaStream_t stream) {
   const size_t smem = tile_bytes<D, NC>() + (a.v.batch + 1) * sizeof(int64_t);
-  cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<D, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  constexpr int kMost = tile_bytes<D, NC>() + (4096 + 1) * 8;
+  cudaError_t e = allow_smem(kv_split_kernel<D, NC>, kMost, done);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv_split_kernel<D, NC>, dim3(a.plan.blocks), dim3(kThreads), smem, stream, 1, a);
   return e != cudaSuccess || a.prefix == nullptr ? e : run_join<D>(a, false, stream);

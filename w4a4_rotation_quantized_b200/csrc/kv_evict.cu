@@ -318,7 +318,8 @@ qr_status launch_kv_evict(const KvView& v, const KvEvictJob& j, cudaStream_t str
     e = launch_pdl(kv_select_kernel<256>, dim3(v.batch, v.groups), dim3(256), static_cast<size_t>(held) * 4, stream, 1, v,
                    j.mass, j.mass_out, j.ld_mass, j.keep, j.recent, j.kept, j.lens_out, held);
   } else {
-    e = cudaFuncSetAttribute(kv_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysHeld * 4);
+    static std::atomic<uint64_t> done{0};
+    e = allow_smem(kv_select_kernel<1024>, kKeysHeld * 4, done);
     if (e == cudaSuccess)
       e = launch_pdl(kv_select_kernel<1024>, dim3(v.batch, v.groups), dim3(1024), static_cast<size_t>(held) * 4, stream,
                      1, v, j.mass, j.mass_out, j.ld_mass, j.keep, j.recent, j.kept, j.lens_out, held);

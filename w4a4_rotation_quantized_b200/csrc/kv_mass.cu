@@ -422,8 +422,8 @@ cudaError_t run_mass(MassArgs& a, cudaStream_t stream) {
   const int64_t rows = (static_cast<int64_t>(v.tokens) * a.gq + v.batch - 1) / v.batch;
   if (rows > kFewRows) {
     const int block = kWarps * Many<D>::kTokens;
-    const cudaError_t e = cudaFuncSetAttribute(kv_mass_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Many<D>::kBytes);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(kv_mass_many_kernel<D>, Many<D>::kBytes, done);
     if (e != cudaSuccess) return e;
     return launch_pdl(kv_mass_many_kernel<D>, dim3(kShare * ((v.capacity + block - 1) / block), v.groups, v.batch),
                       dim3(kThreads), Many<D>::kBytes, stream, kShare, a);
@@ -431,7 +431,8 @@ cudaError_t run_mass(MassArgs& a, cudaStream_t stream) {
   while (a.groups_log2 < 3 && v.groups % (2 << a.groups_log2) == 0) ++a.groups_log2;
   const int block = 32 * kSteps * (kWarps >> a.groups_log2);
   const int smem = kWarps * few_bytes<D>();
-  const cudaError_t e = cudaFuncSetAttribute(kv_mass_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kv_mass_few_kernel<D>, smem, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kv_mass_few_kernel<D>, dim3((v.capacity + block - 1) / block, v.groups >> a.groups_log2, v.batch),
                     dim3(kThreads), smem, stream, 1, a);

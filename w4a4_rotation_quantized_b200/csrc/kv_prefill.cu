@@ -556,7 +556,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
 template <int D>
 cudaError_t run_prefill(const SplitArgs& a, cudaStream_t stream) {
   const int smem = Shape<D>::kBytes + 1024 + (a.v.batch + 1) * static_cast<int>(sizeof(int64_t));
-  cudaError_t e = cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  constexpr int kMost = Shape<D>::kBytes + 1024 + (kMaxBatch + 1) * 8;
+  const cudaError_t e = allow_smem(kv_prefill_kernel<D>, kMost, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kv_prefill_kernel<D>, dim3(a.plan.blocks), dim3(kThreadsP), smem, stream, 1, a,
                     device_status_word());

@@ -1,6 +1,7 @@
 // qr_internal.h -- host-side declarations shared by the library's .cu files.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -38,6 +39,20 @@ cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem,
   cfg.attrs = attr;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
+}
+
+// Lets kernel `k` have up to `bytes` of dynamic shared memory on the current device; asked of the runtime once a
+// device (`done`: a word of the caller's for this kernel and size).
+template <typename K>
+cudaError_t allow_smem(K k, int bytes, std::atomic<uint64_t>& done) {
+  int d = 0;
+  cudaError_t e = cudaGetDevice(&d);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (d & 63);
+  if (d < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && d < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Device address of this device's status word (see qr_device_status).

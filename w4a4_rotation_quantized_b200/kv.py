@@ -96,6 +96,7 @@ class KVSequences:
                              None if block_table is None else block_table.data_ptr(),
                              kv_lens.data_ptr(), None if cu_q is None else cu_q.data_ptr())
         self._args = (ctypes.byref(cache._c), ctypes.byref(self._c))
+        self._workspace = {}                    # bytes of kv_attention's workspace, by (tokens, q_heads)
 
     def _call(self, fn, *args):
         """fn(cache, seqs, *args, stream) on the cache's device and its current stream."""
@@ -241,9 +242,12 @@ def kv_attention(seqs: KVSequences, q: torch.Tensor, causal: bool = True,
         if _overlap(out, q):
             raise ValueError("out must not overlap q")
     lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
-    need = L.qr_kv_attention_workspace(*seqs._args, tokens, q_heads)
-    if need < 0:
-        raise ValueError("sizes outside what the kernels handle")
+    need = seqs._workspace.get((tokens, q_heads))
+    if need is None:
+        need = L.qr_kv_attention_workspace(*seqs._args, tokens, q_heads)
+        if need < 0:
+            raise ValueError("sizes outside what the kernels handle")
+        seqs._workspace[tokens, q_heads] = need
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     seqs._call(L.qr_kv_attention, q.data_ptr(), _ld(q), tokens, q_heads,
                1.0 / math.sqrt(cache.head_dim) if scale is None else scale, 1 if causal else 0,
