@@ -16,6 +16,15 @@ from . import _lib as L
 from .layer import _need_cuda
 
 
+def _stream_of(index: int) -> int:
+    """The current stream of device `index` as an address."""
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# (without the Stream object, which costs a tenth of a small call)
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+
+
 def _need(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, device=None) -> None:
     _need_cuda(t, dtype, name)
     if tuple(t.shape) != shape or not t.is_contiguous():
@@ -103,8 +112,8 @@ class KVSequences:
         i = self._index
         if torch.cuda.current_device() != i:
             with torch.cuda.device(i):
-                return fn(*self._args, *args, torch.cuda.current_stream(i).cuda_stream)
-        return fn(*self._args, *args, torch.cuda.current_stream(i).cuda_stream)
+                return fn(*self._args, *args, _stream_of(i))
+        return fn(*self._args, *args, _stream_of(i))
 
     def _rows(self, t: torch.Tensor, name: str, unit: int) -> None:
         """t: fp16 rows on the cache's device, a multiple of unit wide, at any stride between rows."""
@@ -122,7 +131,8 @@ class KVSequences:
 
 
 def _ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    rows, width = t.shape
+    return t.stride(0) if rows > 1 else max(t.stride(0), width)
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -191,7 +201,7 @@ def kv_append(seqs: KVSequences, q: Optional[torch.Tensor], k: Optional[torch.Te
         raise ValueError(f"the rope must be on {seqs.device}")
     if q is not None:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
             _need(out, torch.float16, tuple(q.shape), "out", seqs.device)
             if any(_overlap(out, t) for t in given):
@@ -213,7 +223,7 @@ def kv_dequantize(seqs: KVSequences, tokens: int) -> tuple[torch.Tensor, torch.T
     heads*head_dim] each: keys (in R3's basis, as the cache holds them) and values."""
     seqs._need_cu()
     cache = seqs.cache
-    k = torch.empty((tokens, cache.width), dtype=torch.float16, device=seqs.device)
+    k = seqs.kv_lens.new_empty((tokens, cache.width), dtype=torch.float16)
     v = torch.empty_like(k)
     seqs._call(L.qr_kv_dequantize, tokens, k.data_ptr(), v.data_ptr())
     return k, v
@@ -234,21 +244,21 @@ def kv_attention(seqs: KVSequences, q: torch.Tensor, causal: bool = True,
     seqs._rows(q, "q", cache.width)
     tokens, q_heads = q.shape[0], q.shape[1] // cache.head_dim
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         seqs._rows(out, "out", cache.width)
         if out.shape != q.shape:
             raise ValueError(f"out must have q's shape {tuple(q.shape)}")
         if _overlap(out, q):
             raise ValueError("out must not overlap q")
-    lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = q.new_empty((tokens, q_heads), dtype=torch.float32) if return_lse else None
     need = seqs._workspace.get((tokens, q_heads))
     if need is None:
         need = L.qr_kv_attention_workspace(*seqs._args, tokens, q_heads)
         if need < 0:
             raise ValueError("sizes outside what the kernels handle")
         seqs._workspace[tokens, q_heads] = need
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    ws = q.new_empty(need, dtype=torch.uint8) if need else None
     seqs._call(L.qr_kv_attention, q.data_ptr(), _ld(q), tokens, q_heads,
                1.0 / math.sqrt(cache.head_dim) if scale is None else scale, 1 if causal else 0,
                out.data_ptr(), _ld(out), None if lse is None else lse.data_ptr(),
@@ -294,8 +304,8 @@ def kv_evict(seqs: KVSequences, mass: torch.Tensor, keep: int, recent: int,
         raise ValueError("keep must be at least 1 and recent in [0, keep]")
     if table_out is not None:
         _need(table_out, torch.int32, (seqs.batch, seqs.max_pages), "table_out", seqs.device)
-    kept = torch.empty((seqs.batch, cache.groups, keep), dtype=torch.int32, device=seqs.device)
-    lens = torch.empty(seqs.batch, dtype=torch.int32, device=seqs.device)
+    kept = seqs.kv_lens.new_empty((seqs.batch, cache.groups, keep))
+    lens = torch.empty_like(seqs.kv_lens)
     mass_out = mass if table_out is None else torch.empty_like(mass)
     seqs._call(L.qr_kv_evict, mass.data_ptr(), mass.shape[2], keep, recent,
                None if table_out is None else table_out.data_ptr(), mass_out.data_ptr(),
