@@ -387,10 +387,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
 
 // Adds up the parts of items that were cut.  JW = 1: one warp a row, its lanes the elements of the head; a block
 // looks after the item that range blockIdx.y is the first to hold and not the last, if there is one, and
-// takes kJoinRows of its rows (token, query head).  JW = 8, for few rows with many parts: one block a row and 32
+// takes 8 `loops` of its rows (token, query head).  JW = 8, for few rows with many parts: one block a row and 32
 // elements, its warps take every eighth part.
-constexpr int kJoinRows = 32;
-
 // The sum over the parts of ranges first, first + JW, .. last (from jw on) of a row: r of head hb of a block.
 template <int D, int JW, int E>
 __device__ __forceinline__ void join_parts(const SplitArgs& a, const Ranges& ranges, int64_t u0, int32_t first,
@@ -447,7 +445,7 @@ __device__ __forceinline__ void join_parts(const SplitArgs& a, const Ranges& ran
 }
 
 template <int D, int JW>
-__global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
+__global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a, int loops) {
   constexpr int E = JW == 1 ? D / 32 : 1;
   __shared__ float acc[JW][32];
   __shared__ float2 ml[JW];
@@ -479,8 +477,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const SplitArgs a) {
     if (first != c || last == c) return;
     const int32_t all_rows = it.rows.here * a.plan.gq;
 #pragma unroll 1
-    for (int s = 0; s < kJoinRows / 8; ++s) {
-      const int32_t k = blockIdx.x * kJoinRows + s * 8 + warp;     // row of the item: head of the block, row of the tile
+    for (int s = 0; s < loops; ++s) {
+      const int32_t k = (blockIdx.x * loops + s) * 8 + warp;     // row of the item: head of the block, row of the tile
       const int32_t hb = k / a.plan.rows, r = k - hb * a.plan.rows, row = it.tile * a.plan.rows + r;
       if (hb >= (1 << a.heads_log2) || row >= all_rows) continue;
       join_parts<D, 1, E>(a, ranges, u0, first, last, 0, hb, r, e0, m, l, o);
@@ -576,11 +574,13 @@ cudaError_t run_join(const SplitArgs& a, bool prefill, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.v.tokens) * a.q_heads;
   const int64_t items = std::max<int64_t>(1, static_cast<int64_t>(a.v.batch) * a.plan.head_blocks);
   if (!prefill && rows <= 8 * sm_count() && a.plan.blocks > 8 * items)
-    return launch_pdl(kv_join_kernel<D, 8>, dim3(static_cast<unsigned>(rows * (D / 32))), dim3(256), 0, stream, 1, a);
+    return launch_pdl(kv_join_kernel<D, 8>, dim3(static_cast<unsigned>(rows * (D / 32))), dim3(256), 0, stream, 1, a, 1);
   const int64_t most = std::min<int64_t>(a.plan.rows, static_cast<int64_t>(a.v.tokens) * a.plan.gq);
   const int64_t all = a.heads_log2 == 0 ? most : static_cast<int64_t>(a.plan.rows) << a.heads_log2;
-  const unsigned blocks = static_cast<unsigned>((all + kJoinRows - 1) / kJoinRows);
-  return launch_pdl(kv_join_kernel<D, 1>, dim3(blocks, a.plan.blocks), dim3(256), 0, stream, 1, a);
+  // (most blocks find that their range cuts nothing: of the many rows of a prompt's item a warp takes four, of few one)
+  const int loops = prefill ? 4 : 1;
+  const unsigned blocks = static_cast<unsigned>((all + 8 * loops - 1) / (8 * loops));
+  return launch_pdl(kv_join_kernel<D, 1>, dim3(blocks, a.plan.blocks), dim3(256), 0, stream, 1, a, loops);
 }
 
 template <int D, int NC>

@@ -8,8 +8,9 @@
 // A token belongs to one warp, which goes through the rows in order: no atomics, equal calls give equal bits.
 //
 // Few rows a key head (single tokens): bound by the bytes of the keys, d/2 + 8 d/g a token and head.  A warp takes
-// one group and 32 tokens at a time, kSteps times, the next ones under way in a ring in shared memory; warps of
-// a block take neighbouring groups of the same tokens.
+// one group and 32 tokens at a time, the next ones under way in a ring in shared memory; warps of a block take
+// neighbouring groups of the same tokens.  A warp has as many pieces as make some four blocks an SM (four pieces: 35.6 us
+// for 32 sequences of up to 4096 tokens, 64/8 heads; 34.6 so, the start of a block being some microseconds).
 // Many rows: a warp keeps 32 tokens' keys as operands in registers (16 where a head is 256 wide) and the block's
 // eight warps go through the query rows together, 64 at a time through shared memory.  Under a causal mask the first
 // tokens meet the most rows, so four blocks, a cluster, share the rows of 256 tokens and the first adds their sums up
@@ -27,7 +28,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSteps = 4;                      // of 32 tokens, of a warp (few rows)
+constexpr int kLeastSteps = 4;                 // of 32 tokens, of a warp, at least (few rows)
 constexpr int kRowsStaged = 64;                // query rows in shared memory (many rows)
 constexpr int kShare = 4;                      // blocks that share the rows (many rows)
 
@@ -41,7 +42,7 @@ struct MassArgs {
   const float* lse;
   float* mass;
   int64_t ld_mass;
-  int32_t groups_log2;                         // groups of a block (few rows)
+  int32_t groups_log2, steps;                  // groups of a block, pieces of a warp (few rows)
 };
 
 // Keys as the A operand: for word w the products with the low and the high nibbles, rows g and g + 8.
@@ -142,33 +143,35 @@ __global__ void __launch_bounds__(kThreads) kv_mass_few_kernel(const MassArgs a)
   grid_dep_launch();
   const int32_t b = blockIdx.z, j = (blockIdx.y << a.groups_log2) + gw;
   const SeqRows rows = seq_rows(v, b);
-  const int32_t first = (blockIdx.x * ws + sw) * (32 * kSteps);
+  const int32_t first = (blockIdx.x * ws + sw) * (32 * a.steps);
   const int32_t all_rows = rows.here * a.gq;
   const int32_t n_seen = all_rows > 0 ? seen(rows, rows.here - 1, a.causal) : 0;
   if (first >= n_seen) return;                           // (warps do not wait for each other)
-  const int pieces = min((n_seen - first + 31) / 32, kSteps) * a.per;      // (tokens, head of the group)
+  const int pieces = min((n_seen - first + 31) / 32, a.steps) * a.per;      // (tokens, head of the group)
 
   auto slot_of = [&](int i) -> int32_t {
     const int32_t t = first + i / a.per * 32 + lane;
     return i < pieces && t < n_seen ? static_cast<int32_t>(kv_slot(v, v.table, b, t)) : -1;
   };
-  uint32_t there[2];
-  auto fill = [&](int i, int32_t slot) {
-    there[i & 1] = __ballot_sync(0xffffffffu, slot >= 0);
+  // starts the copy of piece i; returns which of its tokens are there
+  auto fill = [&](int i, int32_t slot) -> uint32_t {
+    const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
     if (i < pieces) {
       const uint8_t* key = v.codes[0] + (j * a.per + i % a.per) * S::kRow + lane % S::kChunks * 16;
       S::template issue<true, false>(v, key, nullptr, j, max(slot, 0), smem_u32(ring + (i & 1) * S::kBytes), lane);
     }
     cp_async_commit();
+    return there;
   };
-  int32_t slot = slot_of(0), next = slot_of(1);
-  fill(0, slot);
+  int32_t next = slot_of(1);
+  uint32_t ahead = fill(0, slot_of(0));
   const int row_tiles = (all_rows + 7) / 8;
   float sum[2][2];
   int32_t put_tile = -1, put_head = -1;                  // what qf holds
   RowNumbers num{};                                      // of row lane & 7 of that tile
   for (int i = 0; i < pieces; ++i) {
-    fill(i + 1, next);
+    const uint32_t there = ahead;
+    ahead = fill(i + 1, next);
     next = slot_of(i + 2);
     cp_async_wait<1>();
     __syncwarp();
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) kv_mass_few_kernel(const MassArgs a)
     if (i % a.per == 0) sum[0][0] = sum[0][1] = sum[1][0] = sum[1][1] = 0.0f;
     const float* meta = reinterpret_cast<const float*>(st + S::kMeta);
     const KeyNumbers kn = key_numbers(meta[lane], __float_as_int(meta[32 + lane]), a.scale_log2);
-    const bool odd = __any_sync(0xffffffffu, kn.rest != 0.0f) || there[i & 1] != 0xffffffffu;
+    const bool odd = __any_sync(0xffffffffu, kn.rest != 0.0f) || there != 0xffffffffu;
     KeyFrag<D> f[2];
     float sk[2][2], rest[2][2];
     bool is[2][2];
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) kv_mass_few_kernel(const MassArgs a)
         sk[h][e] = __shfl_sync(0xffffffffu, kn.sk, t);
         rest[h][e] = __shfl_sync(0xffffffffu, kn.rest, t);
         z[e] = __shfl_sync(0xffffffffu, kn.z1024, t);
-        is[h][e] = (there[i & 1] >> t) & 1u;
+        is[h][e] = (there >> t) & 1u;
       }
       f[h].load(st, 16 * h, g, c, z[0], z[1]);
     }
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) kv_mass_few_kernel(const MassArgs a)
           x = __shfl_sync(0xffffffffu, x, (lane & 7) * 4);
           if ((lane >> 3) == 2 * h + e) own = x;
         }
-      if ((there[i & 1] >> lane) & 1u) a.mass[(static_cast<int64_t>(b) * v.groups + j) * a.ld_mass + t0 + lane] += own;
+      if ((there >> lane) & 1u) a.mass[(static_cast<int64_t>(b) * v.groups + j) * a.ld_mass + t0 + lane] += own;
     }
     __syncwarp();
   }
@@ -429,7 +432,10 @@ cudaError_t run_mass(MassArgs& a, cudaStream_t stream) {
                       dim3(kThreads), Many<D>::kBytes, stream, kShare, a);
   }
   while (a.groups_log2 < 3 && v.groups % (2 << a.groups_log2) == 0) ++a.groups_log2;
-  const int block = 32 * kSteps * (kWarps >> a.groups_log2);
+  const int step = 32 * (kWarps >> a.groups_log2);
+  const int64_t steps = (static_cast<int64_t>(v.capacity) + step - 1) / step * (v.groups >> a.groups_log2) * v.batch;
+  a.steps = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(steps / (4 * sm_count()), kLeastSteps), 1024));
+  const int block = step * a.steps;
   const int smem = kWarps * few_bytes<D>();
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(kv_mass_few_kernel<D>, smem, done);
