@@ -529,9 +529,12 @@ struct SplitSizes {
 // most kWholePieces pieces a warp.  Elsewhere eight heads a block: warps that read the same tokens' scales
 // share their sectors (one head a block: 64 us instead of 58 for one sequence of 131072 tokens, 64/8 heads).
 constexpr int kWholePieces = 8;
-// Rows of a sequence and key head (on average) up to which the codes go through registers; beyond, through
-// shared memory to tcgen05.
-constexpr int kFewRows = 16;
+// Rows of a sequence and key head (on average) up to which the codes go through registers, 16 rows a tile (8 for heads
+// of 256); beyond, through shared memory to tcgen05, whose time hardly depends on the rows up to 128.
+// Registers against tcgen05, us: 64 sequences of up to 4096 tokens, 64/8 heads: 26 rows 156 and 256, 37 rows 221 and
+// 267, 47 rows 248 and 255; 16 of 2048, 32/32 heads: 23 rows 104 and 175.  With 32 to 64 items of 4096 tokens the tiles'
+// starts and joins weigh more: 16 sequences, 28/4 heads: 16 rows 62 and 51, 29 rows 52 and 52; and 4, 64/8 heads, 48 and 39.
+constexpr int kFewRows = 32;
 
 SplitSizes split_sizes(const KvView& v, int32_t q_heads) {
   SplitSizes s{};

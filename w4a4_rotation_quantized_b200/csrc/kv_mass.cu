@@ -416,8 +416,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_mass_many_kerne
   cluster_sync();
 }
 
-// Rows of a sequence and key head (on average) up to which keys are streamed.
-constexpr int kFewRows = 16;
+// Rows of a sequence and key head (on average) up to which keys are streamed.  Streamed against held, us: 32
+// sequences of up to 4096 tokens, 64/8 heads: 26 rows 85 and 263, 49 rows 141 and 305; 32/32 heads, 31 rows: 458 and
+// 1294; one sequence of 8192, 64/8 heads: 24 rows 20 and 26, 48 rows 35 and 30, 64 rows 44 and 33.
+constexpr int kFewRows = 64;
 
 template <int D>
 cudaError_t run_mass(MassArgs& a, cudaStream_t stream) {
