@@ -1,0 +1,84 @@
+"""What the wrappers of the calls on the paged KV cache hand to the C ABI, without a GPU: host tensors stand in for
+the device's, and the entry points are replaced by ones that note their arguments."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import w4a4_rotation_quantized_b200 as Q
+from w4a4_rotation_quantized_b200 import _lib as L
+from w4a4_rotation_quantized_b200 import kv
+
+
+class Calls(list):
+    """The calls made: (name, arguments)."""
+
+    def take(self, name):
+        def call(*args, **kw):
+            self.append((name, args))
+            return 256
+        return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    made = Calls()
+    monkeypatch.setattr(kv, "_need_cuda", lambda t, dtype, name: None)
+    monkeypatch.setattr(kv, "_stream_of", lambda index: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for name in ("qr_kv_append", "qr_kv_dequantize", "qr_kv_attention", "qr_kv_attention_workspace",
+                 "qr_kv_attention_mass", "qr_kv_evict"):
+        monkeypatch.setattr(L, name, made.take(name))
+    return made
+
+
+def sequences(tokens=5):
+    cache = Q.KVCache.empty(4, 16, 2, 128, device="cpu")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32)
+    return Q.KVSequences(cache, i32([tokens]), i32([0, tokens]), None)
+
+
+def positions_read(c: L.QrKvRope, tokens: int) -> np.ndarray:
+    """The positions that the kernel reads: row of `tokens` at every multiple of ld_pos, one an axis."""
+    got = np.empty((c.axes, tokens), np.int32)
+    for a in range(c.axes):
+        got[a] = np.ctypeslib.as_array((ctypes.c_int32 * tokens).from_address(c.positions + 4 * a * c.ld_pos))
+    return got
+
+
+POSITIONS = {
+    "contiguous": lambda n: torch.arange(3 * n, dtype=torch.int32).reshape(3, n),
+    "expanded": lambda n: torch.arange(n, dtype=torch.int32).unsqueeze(0).expand(3, -1),
+    "expanded rows of two": lambda n: torch.arange(2 * n, dtype=torch.int32).reshape(2, n)[1:].expand(3, -1),
+    "overlapping": lambda n: torch.arange(n + 2, dtype=torch.int32).as_strided((3, n), (1, 1)),
+    "part of wider rows": lambda n: torch.arange(3 * (n + 7), dtype=torch.int32).reshape(3, n + 7)[:, 4:4 + n],
+    "every second row": lambda n: torch.arange(6 * n, dtype=torch.int32).reshape(6, n)[::2],
+    "one axis": lambda n: torch.arange(n, dtype=torch.int32).unsqueeze(0),
+    "one axis, one dimension": lambda n: torch.arange(n, dtype=torch.int32),
+    "one axis of an expanded row": lambda n: torch.arange(n, dtype=torch.int32).expand(1, n),
+}
+
+
+@pytest.mark.parametrize("kind", POSITIONS)
+@pytest.mark.parametrize("tokens", [1, 5])
+def test_positions_of_any_stride_are_read_within_their_storage(calls, kind, tokens):
+    pos = POSITIONS[kind](tokens)
+    want = np.atleast_2d(pos.numpy())
+    rope = Q.Rope(torch.ones(64), torch.zeros(64, dtype=torch.int32))
+    c = rope._c(pos, tokens)
+    assert c.axes == want.shape[0]
+    if c.axes > 1:
+        assert c.ld_pos >= tokens
+        # the last element read lies in the tensor that the struct keeps
+        store = getattr(c, "rows", pos).untyped_storage()
+        end = store.data_ptr() + store.nbytes()
+        assert c.positions + 4 * ((c.axes - 1) * c.ld_pos + tokens) <= end
+    np.testing.assert_array_equal(positions_read(c, tokens), want)
+    # ... and so through the call
+    k = torch.zeros((tokens, 256), dtype=torch.float16)
+    Q.kv_append(sequences(tokens), None, k, k.clone(), rope, pos)
+    (name, args), = calls
+    assert name == "qr_kv_append"
+    assert args[2]._obj.ld_pos == c.ld_pos and args[2]._obj.axes == c.axes
+    np.testing.assert_array_equal(positions_read(args[2]._obj, tokens), want)

@@ -169,11 +169,16 @@ class Rope:
                 or positions.dim() != 2 or positions.shape[1] != tokens
                 or (tokens > 1 and positions.stride(1) != 1)):
             raise ValueError(f"positions must be int32 [axes, {tokens}] rows on {self.inv_freq.device}")
-        if positions.shape[0] == 0:
+        axes = positions.shape[0]
+        if axes == 0:
             raise ValueError("positions must have at least one axis")
-        return L.QrKvRope(self.inv_freq.data_ptr(), None if self.axis is None else self.axis.data_ptr(),
-                          positions.data_ptr(), max(positions.stride(0), tokens),
-                          self.inv_freq.shape[0], positions.shape[0], 1 if self.interleaved else 0)
+        if axes > 1 and positions.stride(0) < tokens:      # one row expanded over the axes, or rows that overlap
+            positions = positions.contiguous()
+        ld = max(positions.stride(0), tokens) if axes == 1 else positions.stride(0)
+        c = L.QrKvRope(self.inv_freq.data_ptr(), None if self.axis is None else self.axis.data_ptr(),
+                       positions.data_ptr(), ld, self.inv_freq.shape[0], axes, 1 if self.interleaved else 0)
+        c.rows = positions                                 # lives until the launch
+        return c
 
 
 def kv_append(seqs: KVSequences, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
@@ -183,7 +188,7 @@ def kv_append(seqs: KVSequences, q: Optional[torch.Tensor], k: Optional[torch.Te
     """Rope and R3 on q and k, and 4-bit codes of k and v into the cache at the newest
     places of the sequences.  q, k, v fp16 [tokens, heads*head_dim] (rows at any stride that is
     a multiple of 8; any may be None); positions int32 [axes, tokens], or [tokens], with a
-    rope.  Returns q with rope and R3 (None without q), the queries of kv_attention.  Rows
+    rope (one row expanded over the axes is copied).  Returns q with rope and R3 (None without q), the queries of kv_attention.  Rows
     outside cu_q's range are left unwritten."""
     given = [t for t in (q, k, v) if t is not None]
     if not given:
