@@ -220,16 +220,17 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
             const uint64_t f2 = f2_pack(f, f);
             l2 = f2_mul(l2, f2);
             zs *= f;
-            const __half2 fh = __float2half2_rn(f);
             tmem_st_wait();
 #pragma unroll 1
-            for (int c = 0; c < ch; ++c) {                 // the weights of this key tile so far
+            for (int c = 0; c < ch; ++c) {                 // the weights of this key tile so far: f in fp32, for a weight
+              // of 2^15 still counts where f is below all of fp16
               uint32_t w[16];
               tmem_ld_32x32b_x16(s_at + 16 * c, w);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(w + i), fh);
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(w + i));
+                const __half2 x = __floats2half2_rn(y.x * f, y.y * f);
                 w[i] = *reinterpret_cast<const uint32_t*>(&x);
               }
               tmem_st_32x32b_x16(s_at + 16 * c, w);
