@@ -43,3 +43,23 @@ def test_a_maximum_that_jumps(d, rows, lag, up):
         c.keys[1][first], c.keys[1][first + 32] = lag, up
         q = np.ones((rows, 256), np.float16)
         check(c, q, [n], [0, rows], None, 1, causal=False, scale=math.log(2) / d)
+
+
+@pytest.mark.parametrize("new,lens", [([1], [1]), ([1, 1], [17, 1]), ([2], [33]), ([1], [300]), ([3, 1], [65, 300]),
+                                      ([40], [300])])
+@pytest.mark.parametrize("spare", [0, 40])                  # a wide table: items are cut instead of taken whole
+@pytest.mark.parametrize("hq,hk,d", [(1, 1, 128), (8, 1, 128), (4, 4, 128), (10, 10, 128), (20, 10, 128), (4, 4, 64),
+                                     (2, 1, 256)])
+@pytest.mark.parametrize("size", [10.0, 30.0, -30.0])
+def test_scores_far_from_zero(hq, hk, d, new, lens, spare, size):
+    """Keys of one sign and queries of one sign: every score is some -100, -300 or +300, and a head's warps that hold
+    none of the tokens, or none that a row sees, must not count with a maximum of 0."""
+    rng = np.random.default_rng(hq * 100 + d + sum(lens))
+    page = 64
+    mp = -(-max(lens) // page) + spare
+    c = R.random_cache(rng, len(new) * mp, page, hk, d, 256 if d == 256 else 128)
+    c.keys[1][:] = rng.uniform(0.08, 0.12, c.keys[1].shape)
+    c.keys[2][:] = 8                                        # c - z in [-16, -1]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q = (size * np.sqrt(128 / d) * rng.uniform(0.9, 1.1, (cu[-1], hq * d))).astype(np.float16)
+    check(c, q, lens, cu, make_table(rng, len(new), mp, c.pages), mp)

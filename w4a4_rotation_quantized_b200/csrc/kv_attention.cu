@@ -357,12 +357,16 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
         const int d2 = e % (D / 2) * 2, hr = e / (D / 2), r = hr % R, h0 = hr / R;
         const int32_t rr = row0 + r;
         if (rr >= all_rows) continue;
+        // a warp that saw no key (l = 0) has no maximum either; a row of NaN has its l
         float mm = -INFINITY;
-        for (int s = 0; s < ws; ++s) mm = fmaxf(mm, all[((s << a.heads_log2) + h0) * R * (D + 2) + r * (D + 2) + D]);
+        for (int s = 0; s < ws; ++s) {
+          const float* from = all + ((s << a.heads_log2) + h0) * R * (D + 2) + r * (D + 2);
+          if (from[D + 1] != 0.0f) mm = fmaxf(mm, from[D]);
+        }
         float ll = 0.0f, y0 = 0.0f, y1 = 0.0f;
         for (int s = 0; s < ws; ++s) {
           const float* from = all + ((s << a.heads_log2) + h0) * R * (D + 2) + r * (D + 2);
-          const float f = from[D] == mm ? 1.0f : exp2_fast(from[D] - mm);
+          const float f = from[D + 1] == 0.0f ? 0.0f : from[D] == mm ? 1.0f : exp2_fast(from[D] - mm);
           ll = fmaf(from[D + 1], f, ll);
           y0 = fmaf(from[d2], f, y0);
           y1 = fmaf(from[d2 + 1], f, y1);
