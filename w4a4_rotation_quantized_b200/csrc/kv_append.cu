@@ -158,10 +158,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 4) kv_append_kernel(const A
 #pragma unroll
           for (int j = 0; j < kLane; j += 4) {
             const float4 cj = c[j / 4], sj = s[j / 4];
-            f2_unpack(f2_add(f2_mul(f2_pack(x[j], x[j + 1]), f2_pack(cj.x, cj.y)),
-                             f2_mul(f2_pack(o[j], o[j + 1]), f2_pack(sj.x, sj.y))), x[j], x[j + 1]);
-            f2_unpack(f2_add(f2_mul(f2_pack(x[j + 2], x[j + 3]), f2_pack(cj.z, cj.w)),
-                             f2_mul(f2_pack(o[j + 2], o[j + 3]), f2_pack(sj.z, sj.w))), x[j + 2], x[j + 3]);
+            // products one by one: those of pairs (f2_mul) were fused into the sum, which is then rounded once only
+            f2_unpack(f2_add(f2_pack(__fmul_rn(x[j], cj.x), __fmul_rn(x[j + 1], cj.y)),
+                             f2_pack(__fmul_rn(o[j], sj.x), __fmul_rn(o[j + 1], sj.y))), x[j], x[j + 1]);
+            f2_unpack(f2_add(f2_pack(__fmul_rn(x[j + 2], cj.z), __fmul_rn(x[j + 3], cj.w)),
+                             f2_pack(__fmul_rn(o[j + 2], sj.z), __fmul_rn(o[j + 3], sj.w))), x[j + 2], x[j + 3]);
           }
         } else {
 #pragma unroll
