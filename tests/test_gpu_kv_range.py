@@ -4,6 +4,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 import w4a4_rotation_quantized_b200 as Q
 from tests import kv_reference as R
@@ -63,3 +64,112 @@ def test_scores_far_from_zero(hq, hk, d, new, lens, spare, size):
     cu = np.concatenate([[0], np.cumsum(new)])
     q = (size * np.sqrt(128 / d) * rng.uniform(0.9, 1.1, (cu[-1], hq * d))).astype(np.float16)
     check(c, q, lens, cu, make_table(rng, len(new), mp, c.pages), mp)
+
+
+class Wide:
+    """A cache made on the device, and float64 attention of some of its rows there."""
+
+    def __init__(self, seqs, n, hk, d, page, seed, key_zero=0, value_zero=-9):
+        self.gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.n, self.hk, self.d, self.page = n, hk, d, page
+        per, w = -(-n // page), hk * d
+        rows = seqs * per * page
+
+        def side(zero):
+            return (torch.randint(0, 256, (rows, w // 2), generator=self.gen, device="cuda", dtype=torch.uint8),
+                    0.05 + 0.1 * torch.rand((rows, w // 128), generator=self.gen, device="cuda"),
+                    torch.full((rows, w // 128), zero, dtype=torch.int32, device="cuda"))
+        self.keys, self.values = side(key_zero), side(value_zero)
+        order = torch.randperm(seqs * per, generator=self.gen, device="cuda").to(torch.int32)
+        self.table = order.reshape(seqs, per).contiguous()
+
+    def sequences(self, lens, cu):
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        cache = Q.KVCache(self.keys, self.values, self.d, 128, self.page)
+        return Q.KVSequences(cache, i32(lens), i32(cu), self.table)
+
+    def wide(self, side, b, n, head):
+        """Values of the first n tokens of a sequence and head: float64 [n, d]."""
+        t = torch.arange(n, device="cuda")
+        slots = self.table[b].long()[t // self.page] * self.page + t % self.page
+        codes, scales, zeros = side
+        d, j = self.d, head * self.d // 128
+        c = codes[slots, head * d // 2:(head + 1) * d // 2]
+        x = torch.stack([c & 15, c >> 4], -1).flatten(1).double()
+        x = torch.where(x > 7, x - 16, x)
+        return (x - zeros[slots, j].double()[:, None]) * scales[slots, j].double()[:, None]
+
+    def attend(self, q, b, head, limits):
+        """out [rows, d], lse [rows], sum of p |v|, largest sum |q k| of rows q [rows, d] that see limits[i] tokens."""
+        n = int(max(limits))
+        k, v = self.wide(self.keys, b, n, head), self.wide(self.values, b, n, head)
+        x = q.double() @ k.T / math.sqrt(self.d)
+        x.masked_fill_(torch.arange(n, device="cuda") >= torch.tensor(limits, device="cuda")[:, None], -math.inf)
+        p = torch.softmax(x, 1)
+        reach = (q.double().abs() @ k.abs().T).amax(1) / math.sqrt(self.d)
+        return p @ v, torch.logsumexp(x, 1), p @ v.abs(), reach
+
+
+@pytest.mark.parametrize("n,causal", [(32768, False), (131072, True)])
+@pytest.mark.parametrize("size", [0.0, 0.02, 1.0])
+def test_prompt_behind_a_long_context(n, causal, size):
+    """A prompt of 2048 behind n tokens, values of one sign, even weights: every block sums tens of thousands of keys, and
+    what such sums lose must stay below what the output's own rounding does.
+
+    Tensor memory sums at most 8192 keys in a row, 512 instructions; one that cuts up to 2^-22 of a sum that grows
+    evenly loses up to 512 2^-22 / 2 = 2^-14 of it, always towards zero.  The output's rounding, up to 2^-11 and of
+    either sign, leaves 2^-11 / sqrt(3 N) of the mean of N outputs, of which four are allowed; so do the weights'
+    roundings, of which there are n more.  l adds 4096 weights in a row in fp32: 4096 / 2 half steps of 2^-24."""
+    hq, hk, d, new = 64, 8, 128, 2048
+    c = Wide(1, n, hk, d, 256, n)
+    q = (size * torch.randn((new, hq * d), generator=c.gen, device="cuda")).half()
+    out, lse = Q.kv_attention(c.sequences([n], [0, new]), q, causal=causal, return_lse=True)
+    rows = [0, 1, 700, 1500, 2047]
+    off, heads = [], [0, 13, 37, 63]
+    for h in heads:
+        at = slice(h * d, (h + 1) * d)
+        want, want_lse, weight, reach = c.attend(q[rows, at], 0, h // 8, [n - new + r + 1 if causal else n for r in rows])
+        got = out[rows, at].double()
+        tol = 2.0 ** -11 * want.abs() + (2.0 ** -11 + 2.0 ** -14 + 4 * (d + 8) * 2.0 ** -24 * reach[:, None]) * weight + 2.0 ** -24
+        assert bool(((got - want).abs() <= tol).all())
+        off.append((got - want) / want)
+        assert bool(((lse[rows, h].double() - want_lse).abs()
+                     <= 2.0 ** -13 + (d + 8) * 2.0 ** -24 * reach + 2.0 ** -22 * want_lse.abs()).all())
+    off = torch.cat(off).flatten()
+    mean = off.mean().item()
+    assert abs(mean) <= 2.0 ** -14 + 4 * 2.0 ** -11 / math.sqrt(3 * off.numel()), f"off by {mean:.3g} on average"
+
+
+@pytest.mark.parametrize("d,hk,gq", [(128, 16, 1), (64, 32, 2), (256, 8, 1)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_items_of_several_sums(d, hk, gq, causal):
+    """Sequences somewhat longer than what is summed in a row, in ranges that hold whole ones and parts: with scores of
+    all sizes, with sequences and rows that see only the first sum's keys, or none."""
+    seqs, n, new = 19, 9000, 40
+    group = 128 if d <= 128 else 256
+    c = Wide(seqs, n, hk, d, 64, d)
+    if d == 256:
+        c.keys, c.values = (tuple(a if i == 0 else a[:, ::2].contiguous() for i, a in enumerate(s)) for s in (c.keys, c.values))
+        c.wide = lambda side, b, m, head, f=c.wide: f((side[0],) + tuple(a.repeat_interleave(2, 1) for a in side[1:]), b, m, head)
+    lens = [n - 37 * b for b in range(seqs)]
+    lens[3], lens[4], lens[5], lens[6] = 8192, 8193, 0, 8200
+    q = 3 * torch.randn((seqs * new, hk * gq * d), generator=c.gen, device="cuda").half()
+    q[::7] *= 0
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    s = Q.KVSequences(Q.KVCache(c.keys, c.values, d, group, c.page), i32(lens), i32(list(range(0, seqs * new + 1, new))), c.table)
+    out, lse = Q.kv_attention(s, q, causal=causal, return_lse=True)
+    again = Q.kv_attention(s, q, causal=causal, return_lse=True)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    for b in range(seqs):
+        rows = slice(b * new, (b + 1) * new)
+        limits = [lens[b] - new + i + 1 if causal else lens[b] for i in range(new)]
+        if lens[b] == 0:
+            assert bool((out[rows] == 0).all()) and bool(torch.isneginf(lse[rows]).all())
+            continue
+        for h in range(0, hk * gq, 3):
+            at = slice(h * d, (h + 1) * d)
+            want, want_lse, weight, reach = c.attend(q[rows, at], b, h // gq, limits)
+            xe = (d + 8) * 2.0 ** -24 * reach
+            tol = 2.0 ** -11 * want.abs() + (2.0 ** -11 + 2.0 ** -14 + 4 * xe[:, None]) * weight + n * 2.0 ** -25 * 3 + 2.0 ** -24
+            assert bool(((out[rows, at].double() - want).abs() <= tol).all()), (b, h)
+            assert bool(((lse[rows, h].double() - want_lse).abs() <= xe + 2.0 ** -13 + 2.0 ** -22 * want_lse.abs()).all())

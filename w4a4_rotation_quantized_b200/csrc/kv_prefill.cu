@@ -45,6 +45,10 @@ constexpr int kSoftmaxThreads = 128;           // of a tile
 constexpr int kUnpackThreads = 128;
 constexpr int kThreadsP = 2 * kSoftmaxThreads + kUnpackThreads + 32;
 constexpr int kMaxBatch = 2048;
+// Steps whose products are summed in tensor memory, 8192 keys.  These sums cut what they are too small for instead of
+// rounding it, some 2^-23.5 of themselves for every 16 keys (measured: 7e-4 of the result after 131072 keys, 1.5e-4
+// after 32768, 4e-5 after 8192, a twelfth of the output's own rounding); chains are added up in fp32.
+constexpr int32_t kChain = 64;
 
 template <int D>
 struct Shape {
@@ -165,9 +169,19 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;            // 32 (warp & 3) in the lane field
     const uint32_t o_at = tmem + lanes + 256 + t * D;
     const int r = 128 * t + (warp & 3) * 32 + lane;
-    for (int32_t done = 0; done < count && ok;) {
-      const Item it = find_item(v, a.plan, prefix, start + done, count - done, &b);
+    // the item's keys that this block takes, in chains: its first unit, its place among the parts, which also keeps the
+    // sums between chains, and m and l so far
+    int32_t run_unit = 0;
+    int run_slot = 0;
+    float run_m = 0.0f, run_l = 0.0f;
+    for (int32_t done = 0, run_end = 0; done < count && ok;) {
+      const Item it = find_item(v, a.plan, prefix, start + done, min(count - done, kChain), &b);
       const int tiles = tiles_of(it);
+      if (done == run_end) {                               // another item
+        run_unit = it.unit;
+        run_slot = done == 0 ? 0 : 1;
+        run_end = done + min(it.units - it.unit, count - done);
+      }
       if (t < tiles) {
         const int32_t row0 = it.tile * a.plan.rows, rr = row0 + r;
         const bool has = rr < it.rows.here * a.plan.gq;
@@ -330,8 +344,26 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
         float l, l1;
         f2_unpack(l2, l, l1);
         l += l1;
-        const int64_t token = it.rows.first + tok, part = part_at(a, blockIdx.x, done == 0 ? 0 : 1, 0, r);
-        const float inv = it.whole ? inverse_or_zero(l) : 1.0f;
+        // an item of several chains: what the ones before it left is added.  A chain that saw no key (l = 0) has no m
+        const bool add = it.unit > run_unit;
+        const bool last = done + it.take == run_end;
+        const bool whole = run_unit == 0 && it.unit + it.take == it.units;
+        float f0 = 0.0f, f1 = 1.0f;
+        if (add) {
+          const float top = fmaxf(run_l != 0.0f ? run_m : -INFINITY, l != 0.0f ? m : -INFINITY);
+          f0 = run_l == 0.0f ? 0.0f : run_m == top ? 1.0f : exp2_fast(run_m - top);
+          f1 = l == 0.0f ? 0.0f : m == top ? 1.0f : exp2_fast(m - top);
+          m = top;
+          l = fmaf(run_l, f0, l * f1);
+        }
+        run_m = m;
+        run_l = l;
+        const int64_t token = it.rows.first + tok, part = part_at(a, blockIdx.x, run_slot, 0, r);
+        if (last && whole) {
+          const float inv = inverse_or_zero(l);
+          f0 *= inv;
+          f1 *= inv;
+        }
         __half* out = a.out + token * a.ldo + qh * D;
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
@@ -347,17 +379,27 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
           float y[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            y[i] = (__uint_as_float(o[(i & 24) + ((i & 3) << 1) + ((i >> 2) & 1)]) - zs) * inv;
-          if (it.whole) {
+            y[i] = (__uint_as_float(o[(i & 24) + ((i & 3) << 1) + ((i >> 2) & 1)]) - zs) * f1;
+          float4* sums = reinterpret_cast<float4*>(a.part_o + part * D + 32 * ch);
+          if (add) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 x = sums[i];
+              y[4 * i] = fmaf(x.x, f0, y[4 * i]);
+              y[4 * i + 1] = fmaf(x.y, f0, y[4 * i + 1]);
+              y[4 * i + 2] = fmaf(x.z, f0, y[4 * i + 2]);
+              y[4 * i + 3] = fmaf(x.w, f0, y[4 * i + 3]);
+            }
+          }
+          if (last && whole) {
             store_half<32>(out + 32 * ch, y);
           } else {
-            float4* to = reinterpret_cast<float4*>(a.part_o + part * D + 32 * ch);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) to[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) sums[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
           }
         }
-        if (has) {
-          if (!it.whole) a.part_ml[part] = make_float2(m, l);
+        if (has && last) {
+          if (!whole) a.part_ml[part] = make_float2(m, l);
           else if (a.lse != nullptr) a.lse[token * a.q_heads + qh] = row_lse(m, l);
         }
       }
@@ -370,7 +412,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
     constexpr int W = P::kWords;
     const int64_t row_bytes = v.width >> 1;
     for (int32_t done = 0; done < count && ok;) {
-      const Item it = find_item(v, a.plan, prefix, start + done, count - done, &b);
+      const Item it = find_item(v, a.plan, prefix, start + done, min(count - done, kChain), &b);
       const int tiles = tiles_of(it);
       const int head = it.block;
       // one token a thread: its key's codes are loaded a step ahead, its value's while the key is unpacked
@@ -492,7 +534,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const SplitArg
     constexpr uint32_t kIdescO = idesc_f16(D) | (1u << 16);            // B with N contiguous
     const uint32_t q0 = smem_u32(q_tile), kv0 = smem_u32(kv_tile);
     for (int32_t done = 0; done < count && ok;) {
-      const Item it = find_item(v, a.plan, prefix, start + done, count - done, &b);
+      const Item it = find_item(v, a.plan, prefix, start + done, min(count - done, kChain), &b);
       const int tiles = tiles_of(it);
       if (lane == 0) {
         // scores of tile t with 64 keys: half `place` of stage st

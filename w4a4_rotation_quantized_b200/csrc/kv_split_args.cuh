@@ -50,7 +50,7 @@ __device__ __forceinline__ float inverse_or_zero(float l) { return l == 0.0f ? 0
 // a sequence at or before the item's, which it becomes (the item's already unless SEARCH).  Called by whole warps.
 struct Item {
   SeqRows rows;
-  int32_t tile, block, unit;                   // tile of rows, block of heads, first unit
+  int32_t tile, block, unit, units;            // tile of rows, block of heads, first unit, units of the whole item
   int32_t take, seen;                          // units to take; tokens that the tile's last row sees
   bool whole;                                  // the item is taken whole
 };
@@ -93,6 +93,7 @@ __device__ __forceinline__ Item find_item(const KvView& v, const SplitPlan& p, c
   it.tile = tile;
   it.block = p.head_blocks == 1 ? 0 : static_cast<int32_t>(static_cast<uint32_t>(off) / static_cast<uint32_t>(tu));
   it.unit = static_cast<int32_t>(off - static_cast<int64_t>(it.block) * tu);
+  it.units = tu;
   it.take = min(tu - it.unit, left);
   it.whole = it.take == tu;
   it.seen = tile_seen(p, it.rows, it.tile);
