@@ -8,8 +8,8 @@ import torch
 
 import w4a4_rotation_quantized_b200 as Q
 from tests import kv_reference as R
-from tests.gpu_helpers import require_gpu
-from tests.test_gpu_kv_attention import check, make_table
+from tests.gpu_helpers import host, require_gpu
+from tests.test_gpu_kv_attention import check, gpu_cache, make_table
 
 pytestmark = pytest.mark.gpu
 
@@ -173,3 +173,29 @@ def test_items_of_several_sums(d, hk, gq, causal):
             tol = 2.0 ** -11 * want.abs() + (2.0 ** -11 + 2.0 ** -14 + 4 * xe[:, None]) * weight + n * 2.0 ** -25 * 3 + 2.0 ** -24
             assert bool(((out[rows, at].double() - want).abs() <= tol).all()), (b, h)
             assert bool(((lse[rows, h].double() - want_lse).abs() <= xe + 2.0 ** -13 + 2.0 ** -22 * want_lse.abs()).all())
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_table_of_no_pages(new):
+    """max_pages = 0 with a table, as the C ABI allows it: nothing is held, whatever the lengths say, and the table has no
+    element to read."""
+    rng = np.random.default_rng(new)
+    c = R.random_cache(rng, 2, 16, 2, 128, 128)
+    cache = gpu_cache(c)
+    lens, cu = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([new, 30], [0, new, 2 * new]))
+    seqs = Q.KVSequences(cache, lens, cu, torch.zeros((2, 0), dtype=torch.int32, device="cuda"))
+    table = torch.zeros(1, dtype=torch.int32, device="cuda")           # the address of an empty table
+    seqs._c.block_table = table.data_ptr()
+    assert seqs.max_pages == 0 and seqs.capacity == 0
+    q = torch.randn((2 * new, 4 * 128), device="cuda").half()
+    out, lse = Q.kv_attention(seqs, q, return_lse=True)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    mass = torch.ones((2, 2, 3), device="cuda")
+    assert bool((Q.kv_attention_mass(seqs, q, lse, mass) == 1).all())
+    before = [a.clone() for a in cache.keys + cache.values]
+    k = torch.randn((2 * new, 2 * 128), device="cuda").half()
+    assert bool(torch.isfinite(Q.kv_append(seqs, q, k, k)).all())
+    assert all(torch.equal(a, b) for a, b in zip(before, cache.keys + cache.values))
+    assert all(bool((a == 0).all()) for a in Q.kv_dequantize(seqs, 2 * new))
+    kept, now, _ = Q.kv_evict(seqs, mass, 2, 1)
+    assert bool((kept == -1).all()) and host(now).tolist() == [0, 0]

@@ -51,7 +51,7 @@ qr_status make_view(const qr_kv_cache* c, const qr_kv_seqs* s, int64_t tokens, b
   v->scales[1] = c->v_scales;
   v->zeros[0] = c->k_zeros;
   v->zeros[1] = c->v_zeros;
-  v->table = s->block_table;
+  v->table = s->max_pages > 0 ? s->block_table : nullptr;   // (a table of no pages has no element to read)
   v->lens = s->kv_lens;
   v->cu = s->cu_q;
   v->pages = static_cast<int32_t>(c->slots / c->page_size);
@@ -194,7 +194,7 @@ qr_status qr_kv_evict(const qr_kv_cache* cache, const qr_kv_seqs* seqs, const fl
     return QR_ERR_INVALID_ARG;
   if (lens_out == v.lens) return QR_ERR_INVALID_ARG;
   // other pages only under a table of their own: without one both would be the same
-  if (table_out != nullptr && table_out == v.table) return QR_ERR_INVALID_ARG;
+  if (table_out != nullptr && table_out == seqs->block_table) return QR_ERR_INVALID_ARG;
   if (!aligned<4>(mass) || !aligned<4>(mass_out) || !aligned<4>(kept) || !aligned<4>(lens_out) ||
       !aligned<4>(table_out))
     return QR_ERR_ALIGNMENT;
