@@ -82,3 +82,12 @@ def test_positions_of_any_stride_are_read_within_their_storage(calls, kind, toke
     assert name == "qr_kv_append"
     assert args[2]._obj.ld_pos == c.ld_pos and args[2]._obj.axes == c.axes
     np.testing.assert_array_equal(positions_read(args[2]._obj, tokens), want)
+
+
+def test_positions_without_a_rope_are_refused(calls):
+    k = torch.zeros((5, 256), dtype=torch.float16)
+    with pytest.raises(ValueError, match="rope"):
+        Q.kv_append(sequences(), None, k, k.clone(), positions=torch.arange(5, dtype=torch.int32))
+    assert not calls
+    Q.kv_append(sequences(), None, k, k.clone())
+    assert len(calls) == 1

@@ -202,6 +202,8 @@ def kv_append(seqs: KVSequences, q: Optional[torch.Tensor], k: Optional[torch.Te
         seqs._rows(t, name, cache.head_dim)
         if t.shape[0] != tokens or (name != "q" and t.shape[1] != cache.width):
             raise ValueError("q, k, v must have the same rows, k and v the cache's width")
+    if rope is None and positions is not None:
+        raise ValueError("positions without a rope")
     if rope is not None and rope.inv_freq.device != seqs.device:
         raise ValueError(f"the rope must be on {seqs.device}")
     if q is not None:
