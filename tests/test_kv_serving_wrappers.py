@@ -91,3 +91,33 @@ def test_positions_without_a_rope_are_refused(calls):
     assert not calls
     Q.kv_append(sequences(), None, k, k.clone())
     assert len(calls) == 1
+
+
+def test_the_workspace_is_asked_for_on_the_caches_device(calls, monkeypatch):
+    """The current device is another one: both the size and the launch belong to the cache's.  One size is kept."""
+    inside = []
+
+    class Device:
+        def __init__(self, i):
+            self.i = i
+
+        def __enter__(self):
+            inside.append(self.i)
+
+        def __exit__(self, *error):
+            inside.append(None)
+
+    seqs = sequences(5)
+    seqs._index = 1
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    seen = []
+    for name in ("qr_kv_attention_workspace", "qr_kv_attention"):
+        monkeypatch.setattr(L, name, lambda *a, name=name: seen.append((name, a, inside[-1] if inside else None)) or 64)
+    for tokens in (5, 5, 3, 5):
+        q = torch.zeros((tokens, 512), dtype=torch.float16)
+        Q.kv_attention(seqs, q)
+    assert [n for n, _, _ in seen] == ["qr_kv_attention_workspace", "qr_kv_attention", "qr_kv_attention"] \
+        + ["qr_kv_attention_workspace", "qr_kv_attention"] * 2
+    assert all(at == 1 for _, _, at in seen)
+    assert all(a[2:] == (tokens, 4) for (n, a, _), tokens in zip([x for x in seen if x[0].endswith("workspace")], (5, 3, 5)))
+    assert seqs._workspace == ((5, 4), 64)

@@ -105,7 +105,7 @@ class KVSequences:
                              None if block_table is None else block_table.data_ptr(),
                              kv_lens.data_ptr(), None if cu_q is None else cu_q.data_ptr())
         self._args = (ctypes.byref(cache._c), ctypes.byref(self._c))
-        self._workspace = {}                    # bytes of kv_attention's workspace, by (tokens, q_heads)
+        self._workspace = None                  # (tokens, q_heads) of the last kv_attention, and its workspace's bytes
 
     def _call(self, fn, *args):
         """fn(cache, seqs, *args, stream) on the cache's device and its current stream."""
@@ -114,6 +114,17 @@ class KVSequences:
             with torch.cuda.device(i):
                 return fn(*self._args, *args, _stream_of(i))
         return fn(*self._args, *args, _stream_of(i))
+
+    def _workspace_bytes(self, tokens: int, q_heads: int) -> int:
+        """Bytes of kv_attention's workspace: the cut of its work, and so they, depend on the cache's device."""
+        last = self._workspace
+        if last is not None and last[0] == (tokens, q_heads):
+            return last[1]
+        need = self._call(lambda c, s, *a: L.qr_kv_attention_workspace(c, s, *a[:-1]), tokens, q_heads)
+        if need < 0:
+            raise ValueError("sizes outside what the kernels handle")
+        self._workspace = (tokens, q_heads), need
+        return need
 
     def _rows(self, t: torch.Tensor, name: str, unit: int) -> None:
         """t: fp16 rows on the cache's device, a multiple of unit wide, at any stride between rows."""
@@ -259,12 +270,7 @@ def kv_attention(seqs: KVSequences, q: torch.Tensor, causal: bool = True,
         if _overlap(out, q):
             raise ValueError("out must not overlap q")
     lse = q.new_empty((tokens, q_heads), dtype=torch.float32) if return_lse else None
-    need = seqs._workspace.get((tokens, q_heads))
-    if need is None:
-        need = L.qr_kv_attention_workspace(*seqs._args, tokens, q_heads)
-        if need < 0:
-            raise ValueError("sizes outside what the kernels handle")
-        seqs._workspace[tokens, q_heads] = need
+    need = seqs._workspace_bytes(tokens, q_heads)
     ws = q.new_empty(need, dtype=torch.uint8) if need else None
     seqs._call(L.qr_kv_attention, q.data_ptr(), _ld(q), tokens, q_heads,
                1.0 / math.sqrt(cache.head_dim) if scale is None else scale, 1 if causal else 0,
