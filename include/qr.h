@@ -548,6 +548,10 @@ QR_API qr_status qr_kv_attention_mass(const qr_kv_cache* cache, const qr_kv_seqs
  *  kept        int32 [batch x W/group x keep]: the place each kept token had, -1
  *              behind the last
  *  lens_out    int32 [batch]: min(n, keep); not kv_lens itself
+ * A token whose page is not in the cache is chosen by its mass like any other (-inf: only when
+ * nothing else is left; the newest stay in any case), and the place that it moves to keeps what it
+ * held: where pages have been given up, give their tokens a mass of -inf and keep no more than are there.
+ * A place whose page is not in the cache receives nothing.
  * 1 <= keep < 2^30, 0 <= recent <= keep.  cu_q is not used. */
 QR_API qr_status qr_kv_evict(const qr_kv_cache* cache, const qr_kv_seqs* seqs, const float* mass,
                              int64_t ld_mass, int32_t keep, int32_t recent,

@@ -199,3 +199,39 @@ def test_a_table_of_no_pages(new):
     assert all(bool((a == 0).all()) for a in Q.kv_dequantize(seqs, 2 * new))
     kept, now, _ = Q.kv_evict(seqs, mass, 2, 1)
     assert bool((kept == -1).all()) and host(now).tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_eviction_with_pages_that_were_given_up(in_place):
+    """Tokens whose page is not in the cache, with a mass of -inf: none stays while others are there, and what stays
+    is moved as if they had never been.  One that stays all the same leaves its place as it was."""
+    rng = np.random.default_rng(1)
+    hk, d, page, mp, n, keep, recent = 2, 128, 16, 6, 90, 40, 10
+    c = R.random_cache(rng, 2 * mp + 1, page, hk, d, 128)
+    table = np.array([[0, -1, 2, 2 * mp + 1, 4, 5]], np.int32)       # pages 1 and 3 are gone: 90 - 32 tokens are there
+    to = np.arange(mp, 2 * mp, dtype=np.int32)[None]
+    if in_place:
+        to = table
+    mass = np.exp(rng.standard_normal((1, hk, mp * page))).astype(np.float32)
+    src = R.slots_of(c, table, mp, 0, mp * page)
+    dst = R.slots_of(c, to, mp, 0, mp * page)
+    mass[:, :, src < 0] = -np.inf
+    for budget in (keep, 70):                                        # 70: twelve that are not there stay too
+        cache = gpu_cache(c)
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        seqs = Q.KVSequences(cache, i32([n]), None, i32(table.tolist()))
+        kept, now, _ = Q.kv_evict(seqs, torch.tensor(mass, device="cuda"), budget, recent,
+                                  None if in_place else i32(to.tolist()))
+        assert host(now).tolist() == [budget]
+        want = [[a.copy() for a in side] for side in (c.keys, c.values)]
+        for j in range(hk):
+            stay = R.evict(mass[0, j], n, budget, recent)
+            assert (src[stay] < 0).sum() == (0 if budget == keep else 12)
+            np.testing.assert_array_equal(host(kept)[0, j], stay)
+            ok = (src[stay] >= 0) & (dst[:budget] >= 0)
+            for side, old in zip(want, (c.keys, c.values)):
+                for a, o, w in zip(side, old, (64, 1, 1)):
+                    a[dst[:budget][ok], j * w:(j + 1) * w] = o[src[stay][ok], j * w:(j + 1) * w]
+        for side, w in zip((cache.keys, cache.values), want):
+            for a, b in zip(side, w):
+                np.testing.assert_array_equal(host(a), b)

@@ -310,7 +310,9 @@ def kv_evict(seqs: KVSequences, mass: torch.Tensor, keep: int, recent: int,
     mass along with them, or, with table_out (int32 like block_table, other pages than
     those being read), into those pages and a mass of their own.  Returns (kept int32 [batch, groups,
     keep]: the place each kept token had, -1 behind the last; lens int32 [batch]:
-    what each sequence holds now; mass).  kv_lens is left as it is."""
+    what each sequence holds now; mass).  kv_lens is left as it is.  Tokens without a page in the cache
+    hold nothing that could move: give them a mass of -inf, and keep no more than are there (the
+    place that one moves to keeps what it held)."""
     cache = seqs.cache
     _need_mass(seqs, mass, "mass")
     if not 1 <= keep or not 0 <= recent <= keep:
