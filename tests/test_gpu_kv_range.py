@@ -235,3 +235,29 @@ def test_eviction_with_pages_that_were_given_up(in_place):
         for side, w in zip((cache.keys, cache.values), want):
             for a, b in zip(side, w):
                 np.testing.assert_array_equal(host(a), b)
+
+
+@pytest.mark.parametrize("batch,rows,hq,hk", [(4096, 1, 2, 2), (2100, 40, 1, 1), (2048, 40, 1, 1)])
+def test_the_largest_batches(batch, rows, hq, hk):
+    """As many sequences as a call takes, and more than the kernel for many rows takes (2048)."""
+    rng = np.random.default_rng(batch)
+    page, mp, d = 16, 3, 128
+    c = R.random_cache(rng, batch * mp, page, hk, d, 128)
+    table = make_table(rng, batch, mp, c.pages)
+    lens = rng.integers(0, 49, batch)
+    i32 = lambda x: torch.tensor(np.asarray(x, np.int32), device="cuda")
+    cu = np.arange(batch + 1) * rows
+    q = rng.standard_normal((batch * rows, hq * d)).astype(np.float16)
+    few = np.concatenate([np.arange(5), [batch // 2, batch - 2, batch - 1]])
+    seqs = Q.KVSequences(gpu_cache(c), i32(lens), i32(cu), i32(table))
+    out, lse = Q.kv_attention(seqs, torch.tensor(q, device="cuda"), return_lse=True)
+    out, lse = host(out).astype(np.float64).reshape(batch, rows, -1)[few], host(lse).reshape(batch, rows, -1)[few]
+    ref = R.attention(c, q.reshape(batch, rows, -1)[few].reshape(-1, hq * d), lens[few], np.arange(9) * rows, table[few], mp)
+    xe = np.repeat((d + 8) * 2.0 ** -24 * ref.reach, d, axis=1)
+    tol = 2.0 ** -11 * np.abs(ref.out) + (2.0 ** -11 + 2.0 ** -16 + 4 * xe) * ref.weight + 2.0 ** -20
+    assert np.all(np.abs(out.reshape(-1, hq * d) - ref.out) <= tol)
+    gone = np.isneginf(ref.lse)
+    lse = lse.reshape(-1, hq)
+    assert np.array_equal(np.isneginf(lse), gone)
+    xe = (d + 8) * 2.0 ** -24 * ref.reach[~gone]
+    assert np.all(np.abs(lse[~gone] - ref.lse[~gone]) <= xe + 2.0 ** -16 + 2.0 ** -22 * np.abs(ref.lse[~gone]))
