@@ -121,3 +121,34 @@ def test_the_workspace_is_asked_for_on_the_caches_device(calls, monkeypatch):
     assert all(at == 1 for _, _, at in seen)
     assert all(a[2:] == (tokens, 4) for (n, a, _), tokens in zip([x for x in seen if x[0].endswith("workspace")], (5, 3, 5)))
     assert seqs._workspace == ((5, 4), 64)
+
+
+def test_overlap_is_that_of_elements():
+    """Columns of one buffer do not overlap; everything that shares an element does.  Against the elements' addresses."""
+    buf = torch.zeros(4096, dtype=torch.float16)
+
+    def elements(t):
+        rows, cols = t.shape
+        return {t.storage_offset() + i * t.stride(0) + j * t.stride(1) for i in range(rows) for j in range(cols)}
+
+    rng = np.random.default_rng(0)
+    views = [buf.as_strided((int(rng.integers(0, 5)), w), (int(rng.choice([p for p in (16, 24, 40) if p >= w])), 1),
+                            int(rng.integers(0, 100))) for w in rng.choice([8, 16, 24], 60)]
+    for a in views:
+        for b in views:
+            shared = bool(elements(a) & elements(b))
+            assert kv._overlap(a, b) or not shared
+            columns = lambda t: {(t.storage_offset() + j) % t.stride(0) for j in range(t.shape[1])}
+            if a.stride(0) == b.stride(0) and not columns(a) & columns(b):
+                assert not kv._overlap(a, b)
+
+
+def test_outputs_beside_the_queries_in_one_buffer(calls):
+    """A wide buffer of rows: queries in some columns, outputs in others."""
+    rows = torch.zeros((5, 1024), dtype=torch.float16)
+    Q.kv_attention(sequences(), rows[:, :512], out=rows[:, 512:])
+    Q.kv_attention(sequences(), rows[:, 512:], out=rows[:, :512])
+    assert sum(n == "qr_kv_attention" for n, _ in calls) == 2
+    for out in (rows[:, :512], rows[:, 256:768], rows[:, 504:1016]):
+        with pytest.raises(ValueError, match="overlap"):
+            Q.kv_attention(sequences(), rows[:, :512], out=out)

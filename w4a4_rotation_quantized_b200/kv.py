@@ -147,13 +147,21 @@ def _ld(t: torch.Tensor) -> int:
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors of rows share an element (or may: rows of unlike pitch that lie between each other)."""
     def span(t):
         first = t.data_ptr()
         return first, first + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
     if a.numel() == 0 or b.numel() == 0:
         return False
     (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
+    if not (a0 < b1 and b0 < a1):
+        return False
+    pitch = a.stride(0)
+    if a.dtype != b.dtype or pitch != b.stride(0) or (b0 - a0) % a.element_size():
+        return True
+    # columns of the same rows: b's begin `at` elements behind a's, or behind those of some other row
+    at = (b0 - a0) // a.element_size() % pitch if pitch > 0 else 0
+    return at < a.shape[1] or at + b.shape[1] > pitch
 
 
 class Rope:
