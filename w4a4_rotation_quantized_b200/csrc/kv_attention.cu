@@ -33,13 +33,11 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-// pieces of a warp's ring
-template <int D>
-constexpr int stages() { return 2; }
+constexpr int kStages = 2;                     // pieces of a warp's ring
 constexpr int kStep = 32;                      // tokens of a piece
 
 template <int D, int NC>
-constexpr int ring_bytes() { return kWarps * (stages<D>() * KvStage<D>::kBytes + KvStage<D>::kPrepared + NC * QueryFrag<D>::kBytes); }
+constexpr int ring_bytes() { return kWarps * (kStages * KvStage<D>::kBytes + KvStage<D>::kPrepared + NC * QueryFrag<D>::kBytes); }
 template <int D, int NC>
 constexpr int join_bytes() { return kWarps * 8 * NC * (D + 2) * 4; }
 template <int D, int NC>
@@ -49,7 +47,7 @@ template <int D, int NC>
 __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_split_kernel(const SplitArgs a) {
   using S = KvStage<D>;
   using T = ValueTile<D>;
-  constexpr int R = 8 * NC, kStages = stages<D>();
+  constexpr int R = 8 * NC;
   extern __shared__ __align__(128) uint8_t smem[];
   const KvView& v = a.v;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

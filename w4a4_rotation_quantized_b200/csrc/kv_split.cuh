@@ -111,9 +111,8 @@ __device__ __forceinline__ void split_prefix(const KvView& v, const SplitPlan& p
   }
 }
 
-// The ranges: `blocks` of them at most, of no fewer than kLeastUnits units; the first
+// The ranges: `blocks` of them at most, of one unit at least; the first
 // `longer` have one unit more.
-constexpr int32_t kLeastUnits = 1;
 struct Ranges {
   int32_t blocks, each, longer;
 
@@ -121,7 +120,7 @@ struct Ranges {
     Ranges r;
     if (units < 0x7FFFFFFF) {                             // (32-bit divisions are several times shorter)
       const uint32_t u = static_cast<uint32_t>(units);
-      r.blocks = min(max(static_cast<int32_t>(u / kLeastUnits), 1), p.blocks);
+      r.blocks = min(max(static_cast<int32_t>(u), 1), p.blocks);
       r.each = static_cast<int32_t>(u / static_cast<uint32_t>(r.blocks));
       r.longer = static_cast<int32_t>(u - static_cast<uint32_t>(r.blocks) * r.each);
     } else {
