@@ -485,7 +485,7 @@ typedef struct {
  *         cache is left as it is
  * Without a rope the results equal qr_kv_quantize's bit for bit.  Pointers
  * 16-byte aligned, ldq, ldk, ldv multiples of 8 (ALIGNMENT otherwise).  q_rot must not overlap
- * Q.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA. */
+ * Q, K or V.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA. */
 QR_API qr_status qr_kv_append(const qr_kv_cache* cache, const qr_kv_seqs* seqs,
                               const qr_kv_rope* rope, const uint16_t* Q, int64_t ldq,
                               const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv,
@@ -512,7 +512,12 @@ QR_API qr_status qr_kv_dequantize(const qr_kv_cache* cache, const qr_kv_seqs* se
  *         and after the call, and calls that may run at the same time need one each
  * Scores, the softmax's maximum and sum and the output's sums are fp32; the weights
  * that meet the values on the tensor cores are rounded to fp16 (a pair of fp16
- * where few rows share a key).
+ * where few rows share a key): with the value's scale in them, to within 2^-11 of themselves or 2^-24 of the
+ * row's largest, whichever is more.  The tensor cores cut what their sums are too small for; no more
+ * than 8192 keys are summed so, which costs up to 2^-14 of sum_t softmax(x)_t |v_t|.
+ * Which kernel runs is chosen for the call as a whole, by its rows of a sequence and key head on
+ * average: results do not depend on it beyond these roundings, but a call that mixes a prompt with single
+ * tokens can take several times what two calls take (qr_kv_attention_mass likewise, up to a hundred times).
  * scale finite; q_heads a multiple of heads, q_heads * head_dim <= 65536. */
 QR_API int64_t qr_kv_attention_workspace(const qr_kv_cache* cache, const qr_kv_seqs* seqs,
                                          int64_t tokens, int32_t q_heads);

@@ -9,7 +9,7 @@
 //
 // 2 (H_q + 2 H_k) d bytes read and 2 H_q d + H_k (d + 16 d / g) written a token, against some 14 operations an
 // element: a lane holds 16 consecutive elements, so that four of the butterfly's stages run in registers (on
-// pairs of fp32) and only those above them by shuffles (103 us for 6200 tokens of 32 + 2 x 32 heads of 128, 276
+// pairs of fp32) and only those above them by shuffles (103 us for 7676 tokens of 32 + 2 x 32 heads of 128, 276
 // with 4 elements a lane: the issue of 250 instructions for 128 elements bound it).  A rope turns (i, i + pairs): the lane reads
 // its elements' partners from memory a second time (they are in L1, since another lane just asked for them), which
 // is cheaper to address than shuffles whose distance depends on the number of pairs.  The angles depend on the

@@ -14,7 +14,7 @@
 // Many rows: a warp keeps 32 tokens' keys as operands in registers (16 where a head is 256 wide) and the block's
 // eight warps go through the query rows together, 64 at a time through shared memory.  Under a causal mask the first
 // tokens meet the most rows, so four blocks, a cluster, share the rows of 256 tokens and the first adds their sums up
-// in order (a prompt of 2048 tokens, 32 heads: 247 us with one block of 8 warps an SM and all rows, 120 so).
+// in order (a prompt of 2048 tokens, 32 heads: 247 us with one block of 8 warps an SM and all rows, 113 so).
 #include <algorithm>
 #include <cmath>
 
@@ -419,6 +419,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) kv_mass_many_kerne
 // Rows of a sequence and key head (on average) up to which keys are streamed.  Streamed against held, us: 32
 // sequences of up to 4096 tokens, 64/8 heads: 26 rows 85 and 263, 49 rows 141 and 305; 32/32 heads, 31 rows: 458 and
 // 1294; one sequence of 8192, 64/8 heads: 24 rows 20 and 26, 48 rows 35 and 30, 64 rows 44 and 33.
+// A batch that mixes both kinds goes one way as a whole: 512 rows on 4096 tokens beside 255 single tokens, 64/8 heads, 33 ms
+// where apart they take 166 and 137 us (24 rows on average: the prompt's 4096 rows of a key head are streamed, 8 at a time).
 constexpr int kFewRows = 64;
 
 template <int D>

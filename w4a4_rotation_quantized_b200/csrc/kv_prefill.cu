@@ -24,10 +24,11 @@
 // items each on its own, so that the next item's queries and first scores are there when the softmax has written
 // the last one's outputs.  Work is shared out and joined as in kv_split.cuh.
 //
-// 2048 new tokens on 8192, 64/8 heads of 128: 842 us, 571 TFLOP/s.  The softmax warps' instructions bound it, by their
-// latency: two of them a scheduler, some 5 instructions a score.  Measured and left: the next 32 columns loaded ahead
-// (890 us: registers), both tiles' rows in one thread (1248 us: half the reads of the columns' numbers, but one
-// softmax warp a scheduler), 128 keys at a time in one place (835 us), the maximum found first (1228 us).
+// 2048 new tokens on 8192, 64/8 heads of 128: 805 us, 597 TFLOP/s.  The softmax warps' instructions bound it, by their
+// latency: two of them a scheduler, some 5 instructions a score.  Measured and left, against 842 us of the
+// kernel as it was then: the next 32 columns loaded ahead (890 us: registers), both tiles' rows in one thread (1248 us: half
+// the reads of the columns' numbers, but one softmax warp a scheduler), the maximum found first (1228 us).  128 keys at a
+// time in one place took 835 us, but with waits that could mistake one completion for the next; it was not made sound.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -246,7 +246,8 @@ def kv_append(seqs: KVSequences, q: Optional[torch.Tensor], k: Optional[torch.Te
 
 def kv_dequantize(seqs: KVSequences, tokens: int) -> tuple[torch.Tensor, torch.Tensor]:
     """The values that the codes of the sequences' newest tokens stand for, fp16 [tokens,
-    heads*head_dim] each: keys (in R3's basis, as the cache holds them) and values."""
+    heads*head_dim] each: keys (in R3's basis, as the cache holds them) and values.  Rows outside
+    cu_q's range are left unwritten."""
     seqs._need_cu()
     cache = seqs.cache
     k = seqs.kv_lens.new_empty((tokens, cache.width), dtype=torch.float16)
@@ -264,7 +265,8 @@ def kv_attention(seqs: KVSequences, q: torch.Tensor, causal: bool = True,
     later ones; otherwise every row sees all kv_lens tokens (cross attention).  scale
     defaults to 1/sqrt(head_dim).  Returns out fp16 like q, and with return_lse the
     log of the softmax's sum, float32 [tokens, q_heads] (-inf, and 0 out, for a row that sees
-    no key).  Rows outside cu_q's range are left unwritten."""
+    no key).  Rows outside cu_q's range are left unwritten.  Prompts and single tokens of one step
+    are better called apart: the kernel is chosen for the call as a whole."""
     seqs._need_cu()
     cache = seqs.cache
     seqs._rows(q, "q", cache.width)
@@ -291,7 +293,8 @@ def kv_attention_mass(seqs: KVSequences, q: torch.Tensor, lse: torch.Tensor, mas
                       causal: bool = True, scale: Optional[float] = None) -> torch.Tensor:
     """Adds to mass (float32 [batch, groups, >= capacity], in place) the attention weight that
     each cached token receives from the rows of q, summed over the rows and the heads of each
-    quantization group; lse as kv_attention returned it for the same rows.  Returns mass."""
+    quantization group; lse as kv_attention returned it for the same rows.  Prompts and single tokens
+    of one step are better called apart.  Returns mass."""
     seqs._need_cu()
     cache = seqs.cache
     seqs._rows(q, "q", cache.width)
