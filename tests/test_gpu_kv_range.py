@@ -261,3 +261,34 @@ def test_the_largest_batches(batch, rows, hq, hk):
     assert np.array_equal(np.isneginf(lse), gone)
     xe = (d + 8) * 2.0 ** -24 * ref.reach[~gone]
     assert np.all(np.abs(lse[~gone] - ref.lse[~gone]) <= xe + 2.0 ** -16 + 2.0 ** -22 * np.abs(ref.lse[~gone]))
+
+
+@pytest.mark.parametrize("batch,hk,rows,n", [(300, 8, 1, 131072), (300, 1, 1, 131072), (3, 8, 4, 131072), (40, 8, 40, 20000)])
+@pytest.mark.parametrize("at", [5, -3])
+@pytest.mark.parametrize("gap", [22.4, 25.4])
+def test_one_heavy_token_before_a_long_even_rest(batch, hk, rows, n, at, gap):
+    """One token outweighs each of the others by 2^gap, and these by their number still count: what the weights' rounding
+    leaves of the rest must not show in fp16.  (All sequences share the same pages.)"""
+    d, page = 128, 1024
+    pages = -(-n // page)
+    full = lambda x, dtype, w: torch.full((pages * page, w), x, dtype=dtype, device="cuda")
+    # every key s_t (1, 1, ..), every value +-1: -1 for the heavy one
+    keys = [full(0x11, torch.uint8, hk * 64), full(0.0, torch.float32, hk), full(0, torch.int32, hk)]
+    values = [full(0x11, torch.uint8, hk * 64), full(1.0, torch.float32, hk), full(0, torch.int32, hk)]
+    keys[1][at % n] = gap
+    values[0][at % n] = 0xff
+    i32 = lambda x: torch.as_tensor(x, dtype=torch.int32, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(batch, -1).contiguous()
+    seqs = Q.KVSequences(Q.KVCache(keys, values, d, 128, page), i32([n] * batch),
+                         i32(np.arange(batch + 1) * rows), table)
+    q = torch.ones((batch * rows, hk * d), device="cuda").half()
+    out, lse = Q.kv_attention(seqs, q, causal=False, scale=math.log(2) / d, return_lse=True)
+    rest = (n - 1) * 2.0 ** -gap
+    want = (rest - 1) / (rest + 1)
+    # one rounding of the output, one of the weights, and 2^-12 of the sum for weights too small for fp16
+    assert (out.double() - want).abs().max().item() <= 2.0 ** -11 * abs(want) + 2.0 ** -11 + 2.0 ** -12
+    # a score of gap ln 2, off by (d + 8) 2^-24 of itself.  l next to the heavy weight, 1 to 2 of it, adds in a row no more
+    # than n / 32 <= 4096 sums of a piece (few rows), or 4096 weights (many rows); each rounds to half a step, 2^-24 of
+    # the heavy weight, which is no less than 2^-24 of l: 2^-12 in all
+    assert (lse.double() - (gap * math.log(2) + math.log1p(rest))).abs().max().item() \
+        <= (d + 8) * 2.0 ** -24 * gap + 2.0 ** -12 + 2.0 ** -18

@@ -8,10 +8,12 @@
 //   x_t = s_k (sum q u - z' sum q) scale log2 e,   z' = z + 8, u = c + 8
 //   o   = sum w_t (c - z),   w_t = s_v 2^(x_t - m),   l = sum 2^(x_t - m).
 // The running maximum m is that of x_t + log2 s_v (with log2 s_v held to [-40, 40]): then the weights that are
-// rounded for the matrix instructions are at most 1 and those that matter are near 1, whatever the values'
-// scales are, and one factor rescales l and o alike.  A weight goes in as two fp16, its rounding and the
+// rounded for the matrix instructions are near 2^7 where they matter, whatever the values' scales are, and one factor
+// rescales l and o alike.  2^7, so that a hundred thousand tokens that are light next to one heavy one, each too small
+// for fp16 next to 1 (2^-25), still add up: at 1 they vanished, 3e-3 of the output where they were 2^-25.4 each.
+// A weight goes in as two fp16, its rounding and the
 // rest: the matrix instructions have room for that (1.5 a token and head).  The maximum is let lag: as long as no
-// weight passes 2^8 nothing is rescaled, and the warp need not even find its maximum.  Zeros of values beyond +-900,
+// weight passes 2^15 nothing is rescaled, and the warp need not even find its maximum.  Zeros of values beyond +-900,
 // which c - z would not survive in fp16, leave a remainder that is summed apart.
 //
 // A warp takes one key head and 32 tokens at a time, its own ring of such pieces in shared
@@ -35,6 +37,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 2;                     // pieces of a warp's ring
 constexpr int kStep = 32;                      // tokens of a piece
+constexpr float kTop = 7.0f, kMost = 15.0f;    // log2 of the largest weight where m is set, and before it is raised
 
 template <int D, int NC>
 constexpr int ring_bytes() { return kWarps * (kStages * KvStage<D>::kBytes + KvStage<D>::kPrepared + NC * QueryFrag<D>::kBytes); }
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
       float over = top[0][0];
 #pragma unroll
       for (int n = 0; n < NC; ++n) over = fmaxf(fmaxf(over, top[n][0]), top[n][1]);
-      if (__any_sync(0xffffffffu, over > 8.0f) || force) {
+      if (__any_sync(0xffffffffu, over > kMost) || force) {
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
           float up[2], f[2];                              // what m grows by
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, s));
             const uint32_t bit = 1u << (2 * n + k);
-            up[k] = started & bit ? fmaxf(y, 0.0f) : y == -INFINITY ? 0.0f : y;
+            up[k] = y == -INFINITY ? 0.0f : started & bit ? fmaxf(y - kTop, 0.0f) : y - kTop;
             f[k] = started & bit ? exp2_fast(-up[k]) : 1.0f;
             if (y != -INFINITY) started |= bit;
             zs[n][k] *= f[k];
@@ -211,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
         }
       }
       uint32_t wh[2][NC][2], wl[2][NC][2], z1024[2][2];
+      uint64_t lp[NC];                                     // the piece's share of l: few additions to a large sum
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
             const float y0 = x[h][n][2 * e], y1 = x[h][n][2 * e + 1];
             float w0, w1;
             const float p0 = exp2_fast(y0), p1 = exp2_fast(y1);
-            l2[n] = f2_add(l2[n], f2_pack(p0, p1));
+            lp[n] = h + e == 0 ? f2_pack(p0, p1) : f2_add(lp[n], f2_pack(p0, p1));
             w0 = p0 * sv;
             w1 = p1 * sv;
             if constexpr (!PLAIN) {
@@ -245,6 +249,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
           }
         }
       }
+#pragma unroll
+      for (int n = 0; n < NC; ++n) l2[n] = f2_add(l2[n], lp[n]);
       value_products<D, NC>(st + S::kCodes, g, c, z1024, wh, wl, o);
     };
 
