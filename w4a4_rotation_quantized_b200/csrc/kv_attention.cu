@@ -350,41 +350,57 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NC == 2 ? 1 : 2) kv_spli
             to[g * T::kPer + T::element(j, false)] = sum_of(j, n, k, false);
             to[g * T::kPer + T::element(j, true)] = sum_of(j, n, k, true);
           }
-          if (g == 0) {
-            to[D] = m[n][k];
-            to[D + 1] = l[n][k];
-          }
+          if (g == 0) *reinterpret_cast<float2*>(to + D) = make_float2(m[n][k], l[n][k]);
         }
       __syncthreads();
-      const float* all = reinterpret_cast<const float*>(smem);
+      // a row's factors, one row a thread, in place of m.  A warp that saw no key (l = 0) has no maximum either; a row of
+      // NaN has its l
+      float* all = reinterpret_cast<float*>(smem);
+      const int next = (R << a.heads_log2) * (D + 2);    // from a head's rows to those of its next warp
+      for (int e = threadIdx.x; e < R << a.heads_log2; e += kThreads) {
+        const int r = e % R, h0 = e / R;
+        const int32_t rr = row0 + r;
+        if (rr >= all_rows) continue;
+        float* at = all + e * (D + 2) + D;
+        float mm = -INFINITY, ll = 0.0f;
+        for (int s = 0; s < ws; ++s) {
+          const float2 ml = *reinterpret_cast<const float2*>(at + s * next);
+          if (ml.y != 0.0f) mm = fmaxf(mm, ml.x);
+        }
+        for (int s = 0; s < ws; ++s) {
+          const float2 ml = *reinterpret_cast<const float2*>(at + s * next);
+          const float f = ml.y == 0.0f ? 0.0f : ml.x == mm ? 1.0f : exp2_fast(ml.x - mm);
+          ll = fmaf(ml.y, f, ll);
+          at[s * next] = f;
+        }
+        at[1] = whole ? inverse_or_zero(ll) : 1.0f;
+        if (!whole) {
+          a.part_ml[part_at(a, blockIdx.x, part, h0, r)] = make_float2(mm, ll);
+        } else if (a.lse != nullptr) {
+          const int h = ((block << a.heads_log2) + h0) * a.plan.gq + rr % a.plan.gq;
+          a.lse[static_cast<int64_t>(rows.first + rr / a.plan.gq) * a.q_heads + h] = row_lse(mm, ll);
+        }
+      }
+      __syncthreads();
       for (int e = threadIdx.x; e < (R << a.heads_log2) * (D / 2); e += kThreads) {
         const int d2 = e % (D / 2) * 2, hr = e / (D / 2), r = hr % R, h0 = hr / R;
         const int32_t rr = row0 + r;
         if (rr >= all_rows) continue;
-        // a warp that saw no key (l = 0) has no maximum either; a row of NaN has its l
-        float mm = -INFINITY;
+        const float* from = all + hr * (D + 2);
+        const float inv = from[D + 1];
+        float y0 = 0.0f, y1 = 0.0f;
         for (int s = 0; s < ws; ++s) {
-          const float* from = all + ((s << a.heads_log2) + h0) * R * (D + 2) + r * (D + 2);
-          if (from[D + 1] != 0.0f) mm = fmaxf(mm, from[D]);
-        }
-        float ll = 0.0f, y0 = 0.0f, y1 = 0.0f;
-        for (int s = 0; s < ws; ++s) {
-          const float* from = all + ((s << a.heads_log2) + h0) * R * (D + 2) + r * (D + 2);
-          const float f = from[D + 1] == 0.0f ? 0.0f : from[D] == mm ? 1.0f : exp2_fast(from[D] - mm);
-          ll = fmaf(from[D + 1], f, ll);
-          y0 = fmaf(from[d2], f, y0);
-          y1 = fmaf(from[d2 + 1], f, y1);
+          const float f = from[s * next + D];
+          const float2 y = *reinterpret_cast<const float2*>(from + s * next + d2);
+          y0 = fmaf(y.x, f, y0);
+          y1 = fmaf(y.y, f, y1);
         }
         if (whole) {
-          const float inv = inverse_or_zero(ll);
           const int64_t token = rows.first + rr / a.plan.gq;
           const int h = ((block << a.heads_log2) + h0) * a.plan.gq + rr % a.plan.gq;
           *reinterpret_cast<__half2*>(a.out + token * a.ldo + h * D + d2) = __floats2half2_rn(y0 * inv, y1 * inv);
-          if (a.lse != nullptr && d2 == 0) a.lse[token * a.q_heads + h] = row_lse(mm, ll);
         } else {
-          const int64_t p = part_at(a, blockIdx.x, part, h0, r);
-          *reinterpret_cast<float2*>(a.part_o + p * D + d2) = make_float2(y0, y1);
-          if (d2 == 0) a.part_ml[p] = make_float2(mm, ll);
+          *reinterpret_cast<float2*>(a.part_o + part_at(a, blockIdx.x, part, h0, r) * D + d2) = make_float2(y0, y1);
         }
       }
       __syncthreads();
